@@ -15,6 +15,14 @@ Operations (the Qwen3.5 linear-attention layer's token mixer):
   decode_layer_step  the whole mixer for one decode token (conv update, SiLU,
                 L2 norm, recurrent step, optional gated RMSNorm) in one kernel.
   gated_rmsnorm the gated RMSNorm output for prefill outputs.
+
+and for the softmax-attention layers between the linear ones, over a paged
+key/value cache (softmax_attention.py):
+  qk_norm_rope  RMSNorm of each query and key head and the rotation by position.
+  qk_norm_rope_cache  the same, keys and values written to the cache.
+  kv_cache, kv_cache_write, kv_cache_read  the cache (e4m3 or bf16).
+  tree_attention  attention of drafted tokens (one: a decode step) over it.
+  kv_cache_accept  the accepted path of a draft moved to its front.
 """
 from __future__ import annotations
 
@@ -26,7 +34,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
-ABI_VERSION = 205  # gdn_version() of the C ABI these argument lists describe
+ABI_VERSION = 300  # gdn_version() of the C ABI these argument lists describe
 
 GDN_F32, GDN_BF16 = 0, 1
 ALGOS = {"auto": 0, "simt": 1, "tensor": 2}
@@ -98,6 +106,24 @@ def lib() -> ctypes.CDLL:
         L.gdn_backward.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32,
                                    f32, i32, f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.gdn_backward.restype = i32
+        L.gdn_qk_norm_rope.argtypes = [vp, vp, i32, i64, i32, i32, i32, i64, i64, vp, vp, f32, vp, vp,
+                                       i32, i32, vp, vp, vp]
+        L.gdn_qk_norm_rope.restype = i32
+        pages = [vp, vp, i32, vp, vp, i32]  # cache, page_table, max_pages, seq_lens, cu_seqlens, N
+        L.gdn_qk_norm_rope_cache.argtypes = [vp, vp, vp, i32, i64, i32, i64, i64, i64, vp, vp, f32, vp, vp,
+                                             i32, i32, *pages, vp, vp]
+        L.gdn_qk_norm_rope_cache.restype = i32
+        L.gdn_kv_write.argtypes = [vp, vp, i32, i64, i64, i64, *pages, vp]
+        L.gdn_kv_write.restype = i32
+        L.gdn_kv_read.argtypes = [*pages, i64, i32, vp, vp, vp]
+        L.gdn_kv_read.restype = i32
+        L.gdn_kv_accept.argtypes = [*pages, vp, i32, vp, vp]
+        L.gdn_kv_accept.restype = i32
+        L.gdn_tree_attention_workspace_size.argtypes = [vp, i32, i32, i32]
+        L.gdn_tree_attention_workspace_size.restype = sz
+        L.gdn_tree_attention.argtypes = [vp, i32, i64, i64, i32, *pages, vp, i32, f32, vp, vp, vp, vp, sz,
+                                         vp]
+        L.gdn_tree_attention.restype = i32
         L.gdn_set_wait_limit_ns.argtypes = [i64]
         L.gdn_set_wait_limit_ns.restype = None
         L.gdn_version.argtypes = []
@@ -464,3 +490,8 @@ def state_bytes(n_layers: int, heads: int, dk: int, dv: int, elem_bytes: int = 4
 def conv_channels(key_heads: int, key_head_dim: int, value_heads: int, value_head_dim: int) -> int:
     """Channels of the fused conv input: q and k (key_dim each) then v."""
     return 2 * key_heads * key_head_dim + value_heads * value_head_dim
+
+
+from .softmax_attention import (KVCache, kv_cache, kv_cache_accept, kv_cache_read, kv_cache_write,  # noqa: E402
+                                qk_norm_rope, qk_norm_rope_cache, rope_inv_freq, tree_attention,
+                                tree_attention_workspace_size, tree_mask)

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "../../include/gdn.h"
+#include "attn.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -55,6 +56,8 @@ gdn_status_t check_host_seqlens(const int32_t* cu, int N, int64_t T_tot) {
 }  // namespace
 
 namespace gdn {
+int* device_status_ptr() { return status_ptr(); }
+
 uint64_t wait_limit_ns() {
     const int64_t v = g_wait_limit_ns.load(std::memory_order_relaxed);
     return v < 0 ? kDefaultWaitNs : static_cast<uint64_t>(v);
@@ -63,10 +66,11 @@ uint64_t wait_limit_ns() {
 
 extern "C" {
 
-// 0.2.5: gdn_prefill_layer_workspace_size; 0.2.4: gdn_prefill_layer; 0.2.3:
+// 0.3.0: the softmax-attention layer (gdn_qk_norm_rope, gdn_qk_norm_rope_cache, gdn_kv_write,
+// gdn_kv_read, gdn_kv_accept, gdn_tree_attention); 0.2.5: gdn_prefill_layer_workspace_size; 0.2.4: gdn_prefill_layer; 0.2.3:
 // gdn_backward_workspace_size_kept; 0.2.2: gdn_prefill_gated; 0.2.1: gdn_set_wait_limit_ns;
 // 0.2.0: Hk, undecayed, gdn_backward
-int gdn_version(void) { return 205; }
+int gdn_version(void) { return 300; }
 
 void gdn_set_wait_limit_ns(int64_t ns) { g_wait_limit_ns.store(ns < 0 ? -1 : ns, std::memory_order_relaxed); }
 

@@ -19,6 +19,18 @@
  *   gdn_gated_rmsnorm  the gated RMSNorm output for prefill outputs.
  *   gdn_backward     gradients of the recurrence (q, k, v, g, beta, h0).
  *
+ * and for the softmax-attention layers that stand between the linear ones, as
+ * a serving loop runs them over a paged key/value cache:
+ *
+ *   gdn_qk_norm_rope        RMSNorm of every query and key head and the
+ *                    rotation by position, in one pass.
+ *   gdn_qk_norm_rope_cache  the same, keys and values written to the cache
+ *                    (quantised where it is) in that pass.
+ *   gdn_kv_write, gdn_kv_read   rows into the cache and back.
+ *   gdn_tree_attention      attention of drafted tokens (a tree, a chain, or
+ *                    the one token of a decode step) over the cache.
+ *   gdn_kv_accept    the accepted path of a draft moved to the front of it.
+ *
  * Sources (page title, section):
  *   [R] "Qwen3.5-MoE source walkthrough", 4.3 Qwen3_5MoeGatedDeltaNet: the
  *       recurrent rule. With the state S stored as [d_k, d_v]:
@@ -35,6 +47,10 @@
  *       a separate projection of the layer input; 7.6.3: RMSNorm(x) =
  *       x / sqrt(mean(x^2) + eps) times a per-feature scale (stored there as
  *       1 + w, zero-centred).
+ *   [A] same page, 7.6.1 (config table) and the layer list: every fourth layer
+ *       is softmax attention with grouped key/value heads, RMSNorm of queries
+ *       and keys per head, a quarter of each head rotated by position (base
+ *       1e7) and a sigmoid gate on the output.
  *   [V] same page, 7.6.1 (config table): the value-head and key-head counts of
  *       the linear-attention layers are separate settings
  *       (linear_num_value_heads, linear_num_key_heads).
@@ -93,7 +109,7 @@ typedef enum {
     GDN_ERR_TIMEOUT = 5       /* a bounded device-side wait ran out */
 } gdn_status_t;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype_t;
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 /* cache values only */ } gdn_dtype_t;
 
 /* Which prefill kernel runs. AUTO picks the tcgen05 tensor-core kernel for
  * bf16 with d_k = d_v = 128 and chunk 64, and the fp32 CUDA-core kernel
@@ -438,6 +454,148 @@ GDN_API gdn_status_t gdn_backward(const void* q, const void* k, const void* v, g
 GDN_API gdn_status_t gdn_gated_rmsnorm(const void* y, const void* z, const float* w, gdn_dtype_t dtype,
                                        int64_t rows, int dv, float eps, void* out, void* stream);
 
+/*
+ * Paged key/value cache of one softmax-attention layer. Position p of a
+ * sequence is row p % page of the page that its page table names at entry
+ * p / page. Values are bf16, or e4m3 with one fp32 scale per (row, head):
+ *   scale = max |x| / 448,  code = x / scale to nearest even;  x ~ code * scale.
+ * A row with an element that is not finite is held as scale NaN and reads back
+ * as NaN; codes are always finite e4m3 values (the two NaN codes are never
+ * written and mean nothing to gdn_tree_attention). An all-zero row has scale 0.
+ *
+ *   k, v               [n_pages, Hk, page, D]  dtype
+ *   k_scale, v_scale   [n_pages, Hk, page]     fp32 (e4m3 only)
+ *   page               tokens of a page: a power of two, 16 to 1024
+ *   D                  a multiple of 16, 16 to 256 (gdn_tree_attention: 64, 128, 256)
+ *
+ * The calls over a cache take, besides it,
+ *   page_table  [N, max_pages] int32   page ids (entries that no position of the
+ *                                      call falls in may hold anything)
+ *   seq_lens    [N] int32              cached tokens of each sequence, the
+ *                                      call's own included
+ *   cu_seqlens  [N+1] int32            the packed tokens of each sequence: they
+ *                                      stand at its last positions, token
+ *                                      cu[n] + i at seq_lens[n] - (cu[n+1] - cu[n]) + i
+ * all on the device. Packed rows behind cu_seqlens[N] are left as they are: not
+ * read into the cache, nor written in the outputs. A position whose page does
+ * not exist (an id outside 0..n_pages-1, or past max_pages) and bounds that make
+ * no sense set the device status word (GDN_ERR_INVALID_ARG); the tokens
+ * concerned are skipped and everything else is done. Sequences may share pages
+ * that a call only reads; a page that a call writes belongs to one sequence.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages;
+    int page;
+    int Hk;
+    int D;
+    gdn_dtype_t dtype; /* GDN_BF16 or GDN_E4M3 */
+} gdn_kv_cache_t;
+
+/*
+ * RMSNorm of each query and key head, then the rotation of its first `rotary`
+ * elements by position. [A]
+ *   y = x / sqrt(mean(x^2) + eps) * w            (w as given; zero-centred: pass 1 + w)
+ *   (a, b) <- (a cos t - b sin t, b cos t + a sin t),  t = positions[token] * inv_freq[i]
+ * for the pairs i = 0 .. rotary/2 - 1: elements (i, i + rotary/2), or
+ * (2i, 2i + 1) when interleaved. Angles are formed and reduced in fp64, the
+ * rest is fp32 with one rounding at the end.
+ *
+ *   q          [T, H, D]   dtype   token stride ld_q elements (0: dense)
+ *   k          [T, Hk, D]  dtype   token stride ld_k
+ *   q_w, k_w   [D]         fp32
+ *   positions  [T]         int32
+ *   inv_freq   [rotary/2]  fp64    radians per position (nullable: rotary 0)
+ *   q_out      [T, H, D]   dtype   dense (may be q itself where q is dense)
+ *   k_out      [T, Hk, D]  dtype   dense (may be k itself where k is dense)
+ * Supported: D a multiple of 16, 16 to 256; rotary a multiple of 16, 0 to D.
+ */
+GDN_API gdn_status_t gdn_qk_norm_rope(const void* q, const void* k, gdn_dtype_t dtype, int64_t T, int H, int Hk,
+                                      int D, int64_t ld_q, int64_t ld_k, const float* q_w, const float* k_w,
+                                      float eps, const int32_t* positions, const double* inv_freq, int rotary,
+                                      int interleaved, void* q_out, void* k_out, void* stream);
+
+/*
+ * The same, with the keys and the values v [T, Hk, D] (token stride ld_v)
+ * written to the cache in that pass instead of k_out: keys are rounded once,
+ * from the fp32 result to the cache's type. q_out rows of skipped tokens are
+ * left as they are.
+ */
+GDN_API gdn_status_t gdn_qk_norm_rope_cache(const void* q, const void* k, const void* v, gdn_dtype_t dtype, int64_t T,
+                                            int H, int64_t ld_q, int64_t ld_k, int64_t ld_v, const float* q_w,
+                                            const float* k_w, float eps, const int32_t* positions,
+                                            const double* inv_freq, int rotary, int interleaved,
+                                            const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,
+                                            const int32_t* seq_lens, const int32_t* cu_seqlens, int N, void* q_out,
+                                            void* stream);
+
+/* Writes k, v [T, Hk, D] (token strides ld_k, ld_v; 0: dense) to the cache. */
+GDN_API gdn_status_t gdn_kv_write(const void* k, const void* v, gdn_dtype_t dtype, int64_t T, int64_t ld_k,
+                                  int64_t ld_v, const gdn_kv_cache_t* cache, const int32_t* page_table,
+                                  int max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens, int N,
+                                  void* stream);
+
+/*
+ * Reads the rows that gdn_kv_write with the same arguments wrote: k, v
+ * [T, Hk, D] dense, of type dtype. With cu_seqlens the running sum of seq_lens
+ * that is the whole of every sequence.
+ */
+GDN_API gdn_status_t gdn_kv_read(const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,
+                                 const int32_t* seq_lens, const int32_t* cu_seqlens, int N, int64_t T,
+                                 gdn_dtype_t dtype, void* k, void* v, void* stream);
+
+/*
+ * Keeps the accepted path of each sequence's draft (its cu[n+1] - cu[n] last
+ * positions): node accepted[n, a] moves to place a of the draft, a = 0, 1, ...,
+ * in place, and new_seq_lens[n] is the length up to the last accepted node. A
+ * row of `accepted` [N, M] int32 holds increasing node numbers and, behind
+ * them, -1s (any negative number); one that does not moves nothing, keeps
+ * seq_lens[n] and sets the device status word. new_seq_lens must not be
+ * seq_lens. Supported: M <= 64.
+ */
+GDN_API gdn_status_t gdn_kv_accept(const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,
+                                   const int32_t* seq_lens, const int32_t* cu_seqlens, int N,
+                                   const int32_t* accepted, int M, int32_t* new_seq_lens, void* stream);
+
+/*
+ * Bytes of device workspace for gdn_tree_attention on the current device (a
+ * multiple of 256); 0 for arguments that it does not support.
+ */
+GDN_API size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, int N, int H, int max_nodes);
+
+/*
+ * Softmax attention of each sequence's drafted tokens over its cached
+ * positions, the drafted ones included (write them first). Query head h reads
+ * key/value head h / (H / Hk). With base = seq_lens[n] - (cu[n+1] - cu[n]), node
+ * i sees every position below base, and base + j where bit j of its mask is set:
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j   (* sigmoid(gate_i)),
+ *   lse_i = log sum_j e^{scale q_i . k_j}.
+ * A row that sees nothing is zero, with lse -infinity. What a row does not see
+ * does not reach it, whatever it holds (infinities and NaN included). fp32
+ * accumulation; the softmax's numerators are rounded to bf16 for the product
+ * with the values. The result does not depend on what else runs, and for one
+ * set of arguments is the same bits at every call.
+ *
+ *   q          [T, H, D]  bf16   token stride ld_q elements (0: dense)
+ *   mask       [T] int64         nullable: a chain (node i sees nodes 0..i)
+ *   gate       [T, H, D]  bf16   nullable, dense
+ *   o          [T, H, D]  bf16   dense
+ *   lse        [T, H]     fp32   nullable
+ *   max_nodes  most drafted tokens of a sequence, 1 to 64: a longer draft is
+ *              skipped and sets the device status word
+ *   workspace  ws_bytes >= gdn_tree_attention_workspace_size(...), 256-byte
+ *              aligned; calls that may overlap need one each
+ * Supported: bf16, D 64, 128 or 256, up to 64 query heads per key/value head.
+ */
+GDN_API gdn_status_t gdn_tree_attention(const void* q, gdn_dtype_t dtype, int64_t T, int64_t ld_q, int H,
+                                        const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,
+                                        const int32_t* seq_lens, const int32_t* cu_seqlens, int N,
+                                        const int64_t* mask, int max_nodes, float scale, const void* gate, void* o,
+                                        float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 GDN_API const char* gdn_status_string(gdn_status_t status);
 
@@ -458,7 +616,8 @@ GDN_API void gdn_set_wait_limit_ns(int64_t ns);
 /*
  * Synchronises `stream`, then reads and clears the device status word that
  * kernels set when they skip work they cannot do safely. Returns GDN_OK,
- * GDN_ERR_INVALID_ARG (a device-side cu_seqlens check failed),
+ * GDN_ERR_INVALID_ARG (a device-side check of cu_seqlens, a page table or an
+ * accepted path failed),
  * GDN_ERR_TIMEOUT (a bounded wait ran out) or GDN_ERR_CUDA.
  */
 GDN_API gdn_status_t gdn_check_device_status(void* stream);
@@ -466,7 +625,8 @@ GDN_API gdn_status_t gdn_check_device_status(void* stream);
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH (0.2.0: q/k head count Hk,
  * the `undecayed` order, gdn_backward; 0.2.1: gdn_set_wait_limit_ns; 0.2.2:
  * gdn_prefill_gated; 0.2.3: gdn_backward_workspace_size_kept; 0.2.4:
- * gdn_prefill_layer; 0.2.5: gdn_prefill_layer_workspace_size). Argument
+ * gdn_prefill_layer; 0.2.5: gdn_prefill_layer_workspace_size; 0.3.0: the
+ * softmax-attention layer's calls and gdn_kv_cache_t). Argument
  * lists change between minor versions; a binding checks the version before
  * calling anything else. */
 GDN_API int gdn_version(void);

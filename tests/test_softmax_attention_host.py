@@ -1,0 +1,212 @@
+"""Host-side checks of the softmax-attention layer's calls (no GPU needed):
+every C entry point refuses bad arguments before it touches a device, the
+binding refuses bad tensors, and the helpers are right."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_deltanet_linear_silu_b200 as gdn
+from gated_deltanet_linear_silu_b200 import build as gbuild
+from gated_deltanet_linear_silu_b200.softmax_attention import _CacheStruct, _cache_arg, _pages
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+A = 1 << 20  # aligned, never dereferenced: validation fails first
+B = 1 << 21
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def L():
+    gbuild.build()
+    return gdn.lib()
+
+
+def cache(**kw):
+    a = dict(k=A, v=A, k_scale=A, v_scale=A, n_pages=4, page=16, Hk=2, D=64, dtype=2)
+    a.update(kw)
+    return ctypes.byref(_CacheStruct(*a.values()))
+
+
+def pages(**kw):
+    a = dict(cache=cache(), table=A, max_pages=2, lens=A, cu=A, N=1)
+    a.update({x: y for x, y in kw.items() if x in a})
+    return list(a.values())
+
+
+BAD_CACHE = [
+    (dict(n_pages=0), INVALID), (dict(n_pages=-1), INVALID), (dict(Hk=0), INVALID), (dict(k=None), INVALID),
+    (dict(v=A + 8), INVALID), (dict(k_scale=None), INVALID), (dict(v_scale=A + 4), INVALID),
+    (dict(dtype=0), INVALID), (dict(dtype=3), INVALID), (dict(page=8), UNSUPPORTED), (dict(page=48), UNSUPPORTED),
+    (dict(page=2048), UNSUPPORTED), (dict(page=0), UNSUPPORTED), (dict(page=-16), UNSUPPORTED),
+    (dict(D=24), UNSUPPORTED), (dict(D=272), UNSUPPORTED), (dict(D=0), UNSUPPORTED),
+]
+BAD_PAGES = [(dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(cu=None), INVALID),
+             (dict(max_pages=0), INVALID), (dict(max_pages=-1), INVALID), (dict(N=-1), INVALID)]
+FROM_PAGES = [(dict(cache=cache(**kw)), st) for kw, st in BAD_CACHE] + [(dict(cache=None), INVALID)] + BAD_PAGES
+
+
+def norm_rope(L, **kw):
+    a = dict(q=A, k=A, dt=1, T=3, H=4, Hk=2, D=64, ldq=0, ldk=0, qw=A, kw=A, eps=1e-6, pos=A, f=A, rot=32, il=0,
+             qo=B, ko=2 * B, stream=None)
+    a.update(kw)
+    return L.gdn_qk_norm_rope(*a.values())
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(T=1 << 31), UNSUPPORTED), (dict(H=0), INVALID),
+    (dict(Hk=0), INVALID), (dict(D=8), UNSUPPORTED), (dict(D=72), UNSUPPORTED), (dict(D=512), UNSUPPORTED),
+    (dict(q=None), INVALID), (dict(k=A + 2), INVALID), (dict(qw=None), INVALID), (dict(kw=None), INVALID),
+    (dict(pos=None), INVALID), (dict(f=None), INVALID), (dict(rot=66), INVALID), (dict(rot=-2), INVALID),
+    (dict(rot=24), UNSUPPORTED), (dict(il=2), INVALID), (dict(eps=NAN), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(ldq=255), INVALID), (dict(ldk=130), INVALID), (dict(qo=None), INVALID), (dict(ko=None), INVALID),
+    (dict(qo=A, ldq=512), INVALID), (dict(ko=A, ldk=256), INVALID), (dict(qo=B, ko=B), INVALID),
+    (dict(qo=B + 8), INVALID),
+])
+def test_qk_norm_rope_refuses(L, kw, expect):
+    assert norm_rope(L, **kw) == expect
+
+
+def rope_cache(L, **kw):
+    a = dict(q=A, k=A, v=A, dt=1, T=3, H=4, ldq=0, ldk=0, ldv=0, qw=A, kw=A, eps=1e-6, pos=A, f=A, rot=32, il=0)
+    a.update({x: y for x, y in kw.items() if x in a})
+    return L.gdn_qk_norm_rope_cache(*a.values(), *pages(**kw), kw.get("qo", B), None)
+
+
+@pytest.mark.parametrize("kw,expect", FROM_PAGES + [
+    (dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(T=1 << 31), UNSUPPORTED), (dict(N=0), INVALID),
+    (dict(v=None), INVALID), (dict(v=A + 8), INVALID), (dict(ldv=8), INVALID), (dict(rot=80), INVALID),
+    (dict(H=0), INVALID), (dict(qo=None), INVALID), (dict(qo=A, ldq=512), INVALID), (dict(pos=None), INVALID),
+])
+def test_qk_norm_rope_cache_refuses(L, kw, expect):
+    assert rope_cache(L, **kw) == expect
+
+
+def write(L, **kw):
+    a = dict(k=A, v=A, dt=1, T=3, ldk=0, ldv=0)
+    a.update({x: y for x, y in kw.items() if x in a})
+    return L.gdn_kv_write(*a.values(), *pages(**kw), None)
+
+
+@pytest.mark.parametrize("kw,expect", FROM_PAGES + [
+    (dict(dt=2), INVALID), (dict(T=-2), INVALID), (dict(k=None), INVALID), (dict(v=A + 4), INVALID),
+    (dict(ldk=64), INVALID), (dict(ldv=129), INVALID), (dict(N=0), INVALID),
+])
+def test_kv_write_refuses(L, kw, expect):
+    assert write(L, **kw) == expect
+
+
+def read(L, **kw):
+    a = dict(T=3, dt=1, k=A, v=B)
+    a.update({x: y for x, y in kw.items() if x in a})
+    return L.gdn_kv_read(*pages(**kw), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", FROM_PAGES + [
+    (dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(k=None), INVALID), (dict(v=A), INVALID),
+    (dict(v=B + 8), INVALID), (dict(N=0), INVALID),
+])
+def test_kv_read_refuses(L, kw, expect):
+    assert read(L, **kw) == expect
+
+
+def accept(L, **kw):
+    a = dict(path=A, M=4, out=B)
+    a.update({x: y for x, y in kw.items() if x in a})
+    return L.gdn_kv_accept(*pages(**kw), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", FROM_PAGES + [
+    (dict(M=-1), INVALID), (dict(M=65), UNSUPPORTED), (dict(path=None), INVALID), (dict(out=None), INVALID),
+    (dict(out=A), INVALID),  # the new lengths must not be the old ones
+])
+def test_kv_accept_refuses(L, kw, expect):
+    assert accept(L, **kw) == expect
+
+
+def attend(L, **kw):
+    a = dict(q=A, dt=1, T=3, ldq=0, H=4)
+    b = dict(mask=A, nodes=8, scale=0.1, gate=None, o=B, lse=None, ws=A, bytes=1 << 40)
+    for x in (a, b):
+        x.update({i: y for i, y in kw.items() if i in x})
+    return L.gdn_tree_attention(*a.values(), *pages(**kw), *b.values(), None)
+
+
+@pytest.mark.parametrize("kw,expect", FROM_PAGES + [
+    (dict(dt=0), UNSUPPORTED), (dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID),
+    (dict(H=3), INVALID), (dict(H=130), UNSUPPORTED), (dict(nodes=0), INVALID), (dict(nodes=65), UNSUPPORTED),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(cache=cache(D=96)), UNSUPPORTED), (dict(q=None), INVALID),
+    (dict(o=None), INVALID), (dict(o=A), INVALID), (dict(q=A + 8), INVALID), (dict(gate=A + 2), INVALID),
+    (dict(gate=B), INVALID), (dict(mask=A + 4), INVALID), (dict(lse=A + 2), INVALID), (dict(ldq=128), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=A + 16), WORKSPACE), (dict(bytes=256), WORKSPACE), (dict(N=0), INVALID),
+])
+def test_tree_attention_refuses(L, kw, expect):
+    assert attend(L, **kw) == expect
+
+
+def test_empty_calls_do_nothing(L):
+    empty = dict(N=0, table=None, lens=None, cu=None)
+    assert norm_rope(L, T=0, q=None, k=None) == OK
+    assert rope_cache(L, T=0, q=None, k=None, v=None, **empty) == OK
+    assert write(L, T=0, k=None, v=None, **empty) == OK
+    assert read(L, T=0, k=None, v=None, **empty) == OK
+    assert accept(L, path=None, out=None, **empty) == OK
+    assert attend(L, T=0, q=None, o=None, ws=None, **empty) == OK
+
+
+def test_workspace_size(L):
+    size = lambda c, N, H, nodes: L.gdn_tree_attention_workspace_size(c, N, H, nodes)
+    assert size(cache(), 4, 8, 8) > 0 and size(cache(), 4, 8, 8) % 256 == 0
+    assert size(cache(), 4096, 8, 8) > size(cache(), 4, 8, 8)
+    assert size(None, 4, 8, 8) == size(cache(D=96), 4, 8, 8) == size(cache(), 4, 8, 0) == size(cache(), -1, 8, 8) == 0
+
+
+def test_binding_refuses_tensors():
+    t = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d)
+    f8, f32, i32, i64 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
+    with pytest.raises(ValueError):  # host tensors
+        _cache_arg(gdn.KVCache(t(2, 1, 16, 64), t(2, 1, 16, 64)))
+    with pytest.raises(ValueError):  # k and v alike
+        _cache_arg(gdn.KVCache(t(2, 1, 16, 64), t(2, 1, 16, 128)))
+    with pytest.raises(ValueError):  # an e4m3 cache has scales
+        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f8), t(2, 1, 16, 64, d=f8)))
+    with pytest.raises(TypeError):
+        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f8), t(2, 1, 16, 64, d=f8), t(2, 1, 16), t(2, 1, 16)))
+    with pytest.raises(TypeError):
+        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f32), t(2, 1, 16, 64, d=f32)))
+    with pytest.raises(TypeError):
+        gdn.kv_cache(2, 16, 1, 64, dtype=f32, device="cpu")
+    with pytest.raises(TypeError):
+        _pages(t(1, 2, d=i64), t(1, d=i32), t(2, d=i32))
+    with pytest.raises(ValueError):
+        _pages(t(2, 2, d=i32), t(1, d=i32), t(2, d=i32))
+    q, k, w = t(3, 4, 64), t(3, 2, 64), t(64, d=f32)
+    pos, f = t(3, d=i32), t(16, d=torch.float64)
+    for bad in [(q, t(2, 2, 64), w, w, pos, f), (q, k.float(), w, w, pos, f), (q, k, w.double(), w, pos, f),
+                (q, k, w, t(32, d=f32), pos, f), (q, k, w, w, pos.long(), f), (q, k, w, w, pos, f.float()),
+                (q, k, w, w, pos, t(33, d=torch.float64)), (q, k, w, w, pos, f)]:  # the last: host tensors
+        with pytest.raises(ValueError):
+            gdn.qk_norm_rope(*bad)
+
+
+def test_tree_mask():
+    #   0        0
+    #  / \       |
+    # 1   2      1      and an empty draft between
+    # |
+    # 3
+    mask, depth = gdn.tree_mask(torch.tensor([-1, 0, 0, 1, -1, 0]), torch.tensor([0, 4, 4, 6]))
+    assert mask.tolist() == [0b1, 0b11, 0b101, 0b1011, 0b1, 0b11]
+    assert depth.tolist() == [0, 1, 1, 2, 0, 1]
+    chain, depth = gdn.tree_mask(torch.arange(-1, 63), torch.tensor([0, 64]))
+    assert chain.tolist() == [(1 << i + 1) - 1 for i in range(63)] + [-1] and depth.tolist() == list(range(64))
+    for parents, cu in [([0], [0, 1]), ([-1, 1], [0, 2]), ([-2], [0, 1]), ([-1] * 65, [0, 65]), ([-1], [0, 2])]:
+        with pytest.raises(ValueError):
+            gdn.tree_mask(torch.tensor(parents), torch.tensor(cu))
+
+
+def test_rope_inv_freq():
+    f = gdn.rope_inv_freq(64)
+    assert f.dtype == torch.float64 and f.numel() == 32 and f[0] == 1.0
+    assert abs(f[16].item() - 1e7 ** -0.5) < 1e-18
