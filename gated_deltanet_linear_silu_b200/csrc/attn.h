@@ -95,8 +95,13 @@ struct TreeArgs {
     float* lse;        // [T, H] or null
     void* workspace;
     int* status;
+    uint64_t wait_ns;  // bound on each wait of the tcgen05 kernel
+    // the launch's plan (launch_tree_attention)
+    int grid, row_tiles, slot_rows, min_tiles;
 };
 size_t tree_workspace_bytes(int N, int H, int Hk, int D, int max_nodes, int e4m3);
+// The tcgen05 kernel alone, for a planned launch.
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace gdn

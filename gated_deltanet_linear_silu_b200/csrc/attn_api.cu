@@ -2,6 +2,7 @@
 // argument validation on the host and dispatch. No allocation, no host sync.
 #include "../../include/gdn.h"
 #include "attn.h"
+#include "launch.h"
 
 namespace {
 
@@ -177,6 +178,7 @@ gdn_status_t gdn_tree_attention(const void* q, gdn_dtype_t dtype, int64_t T, int
     if (dtype != GDN_BF16 || max_nodes > gdn::kMaxNodes) return GDN_ERR_UNSUPPORTED;
     if (!(a.c.D == 64 || a.c.D == 128 || a.c.D == 256) || H / a.c.Hk > 64) return GDN_ERR_UNSUPPORTED;
     if ((int64_t)N * a.c.Hk >= (int64_t)1 << 31) return GDN_ERR_UNSUPPORTED;
+    if (a.c.n_pages >= ((int64_t)1 << 31) / ((int64_t)a.c.Hk << a.c.page_shift)) return GDN_ERR_UNSUPPORTED;
     if (T == 0) return GDN_OK;
     if (!q || !o || o == q || !aligned(q, 16) || !aligned(o, 16) || !aligned(gate, 16) || !aligned(mask, 8) ||
         !aligned(lse, 4) || (gate && gate == o))
@@ -186,7 +188,7 @@ gdn_status_t gdn_tree_attention(const void* q, gdn_dtype_t dtype, int64_t T, int
         ws_bytes < gdn_tree_attention_workspace_size(cache, N, H, max_nodes))
         return GDN_ERR_WORKSPACE;
     a.q = q; a.ld_q = ld_q; a.T = T; a.H = H; a.mask = mask; a.max_nodes = max_nodes; a.scale = scale; a.gate = gate;
-    a.o = o; a.lse = lse; a.workspace = workspace;
+    a.o = o; a.lse = lse; a.workspace = workspace; a.wait_ns = gdn::wait_limit_ns();
     a.status = gdn::device_status_ptr();
     if (!a.status) return GDN_ERR_CUDA;
     return from_cuda(gdn::launch_tree_attention(a, static_cast<cudaStream_t>(stream)));

@@ -32,6 +32,7 @@
 
 #include "kv_page.cuh"
 #include "launch.h"
+#include "tree_attn.cuh"
 
 namespace gdn {
 namespace {
@@ -39,102 +40,12 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRows = 16;           // query rows of a unit
 constexpr int kTile = 16 * kWarps;  // tokens of a tile: 16 per warp
-constexpr int kMinTiles = 2;        // tiles of a CTA's share, at least
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -__builtin_huge_valf();
-
-__device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// bf16x2 of the two e4m3 codes in the high bytes of x's halves: sign to sign,
-// the other seven bits four places down, which leaves the value times 2^-120
-// (subnormals included); the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t x) {
-    const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-    uint32_t z;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x7B807B80u));  // 2^120
-    return z;
-}
-
-__device__ __forceinline__ void cp_async_zfill16(void* dst, const void* src, bool on) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int n = on ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_zfill8(void* dst, const void* src, bool on) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int n = on ? 8 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_zfill4(void* dst, const void* src, bool on) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int n = on ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Sequence n's draft and length, checked; nodes 0 where there is nothing to do.
-struct Seq {
-    int first, nodes, len;  // first packed token, drafted tokens, cached tokens
-    bool bad;
-};
-__device__ __forceinline__ Seq load_seq(const TreeArgs& a, int n) {
-    Seq q;
-    q.first = a.p.cu[n];
-    const int64_t nodes = (int64_t)a.p.cu[n + 1] - q.first;
-    q.len = a.p.lens[n];
-    q.bad = q.first < 0 || nodes < 0 || a.p.cu[n + 1] > a.T || nodes > a.max_nodes || q.len < nodes ||
-            q.len > ((int64_t)a.p.max_pages << a.c.page_shift);
-    q.nodes = q.bad ? 0 : (int)nodes;
-    return q;
-}
-
-// The line of work: unit (n, hk, rt), rt fastest, then tiles of each.
-struct Line {
-    int64_t units, tiles;  // of one sequence: units, tiles per unit
-    __device__ __forceinline__ int64_t total() const { return units * tiles; }
-};
-__device__ __forceinline__ Line seq_line(const TreeArgs& a, const Seq& q) {
-    Line x;
-    const int G = a.H / a.c.Hk;
-    x.units = q.nodes ? (int64_t)a.c.Hk * ((q.nodes * G + kRows - 1) / kRows) : 0;
-    x.tiles = (q.len + kTile - 1) / kTile;
-    return x;
-}
-// Shares: CTA c of C has tiles [c * total / C, (c + 1) * total / C).
-__device__ __forceinline__ int64_t share_count(int64_t total, int grid) {
-    const int64_t c = total / kMinTiles;
-    return c < 1 ? 1 : c < grid ? c : grid;
-}
-__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t C) { return c * total / C; }
-__device__ __forceinline__ int64_t share_of(int64_t tile, int64_t total, int64_t C) {
-    return ((tile + 1) * C - 1) / total;
-}
-
-// Workspace: the line's start of every sequence and its end (int64 [N + 1]),
-// then per CTA two partials (a segment that begins at the CTA's first tile, one
-// that begins later), each m [16], l [16], o [16][D].
-__host__ __device__ inline size_t line_bytes(int N) { return ((size_t)(N + 1) * 8 + 255) / 256 * 256; }
-__host__ __device__ inline size_t slot_floats(int D) { return (size_t)kRows * (D + 2); }
 
 template <int D, bool E4M3>
 struct Config {
@@ -171,87 +82,22 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
     constexpr int kSteps = D / 16;
     constexpr bool kQInSmem = D == 256;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sh_scan[kWarps], sh_find[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
-    const int N = a.p.N, G = a.H / a.c.Hk;
+    const int G = a.H / a.c.Hk;
     pdl_launch_dependents();
 
-    // ---- this CTA's share of the line
-    int64_t* line = static_cast<int64_t*>(a.workspace);
-    int64_t mine = 0;
-    for (int n = tid; n < N; n += kThreads) {
-        const Seq q = load_seq(a, n);
-        if (q.bad && blockIdx.x == 0) set_status(a.status, kStatusBadSeqlens);
-        mine += seq_line(a, q).total();
-    }
-    auto warp_sum64 = [](int64_t x) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        return x;
-    };
-    mine = warp_sum64(mine);
-    if (lane == 0) sh_scan[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kWarps; ++w) total += sh_scan[w];
-    const int64_t shares = share_count(total, gridDim.x);
-    const bool idle = total == 0 || blockIdx.x >= shares;
-    const int64_t begin = idle ? 0 : share_start(blockIdx.x, total, shares);
-    const int64_t end = idle ? 0 : share_start(blockIdx.x + 1, total, shares);
-    if (blockIdx.x == 0 && tid == 0) line[N] = total;
-    if (tid == 0) sh_find[0] = N;
-    __syncthreads();
-    // the sequence that holds tile `begin` (CTA 0 goes on to write every start)
-    int64_t before = 0;
-    for (int n0 = 0; n0 < N; n0 += kThreads) {
-        const int n = n0 + tid;
-        const int64_t own_tiles = n < N ? seq_line(a, load_seq(a, n)).total() : 0;
-        int64_t x = own_tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) sh_scan[warp] = x;
-        __syncthreads();
-        int64_t pre = before;
-        for (int w = 0; w < warp; ++w) pre += sh_scan[w];
-        const int64_t start = pre + x - own_tiles;
-        if (blockIdx.x == 0 && n < N) line[n] = start;
-        if (!idle && own_tiles > 0 && start <= begin && begin < start + own_tiles) {
-            sh_find[0] = n;
-            sh_find[1] = start;
-        }
-        for (int w = 0; w < kWarps; ++w) before += sh_scan[w];
-        __syncthreads();
-        if (blockIdx.x != 0 && sh_find[0] < N) break;
-    }
-    if (idle) return;
-    int n = (int)sh_find[0];
-    int64_t n_start = sh_find[1];
+    const Share share = find_share<kRows, kTile, kThreads>(a);
 
-    float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + line_bytes(N));
+    float* partials = partial_base(a);
     uint8_t* ring = smem + warp * C::kStages * C::kStage;
     uint32_t* q_smem = reinterpret_cast<uint32_t*>(smem + C::kSmem - (kQInSmem ? kSteps * 512 : 0));
 
-    int64_t at = begin;
-    Seq seq = load_seq(a, n);
-    Line ln = seq_line(a, seq);
-    while (at < end) {
-        while (at >= n_start + ln.total()) {  // the next sequence with work
-            n_start += ln.total();
-            ++n;
-            seq = load_seq(a, n);
-            ln = seq_line(a, seq);
-        }
-        const int64_t unit = (at - n_start) / ln.tiles;
-        const int64_t unit_start = n_start + unit * ln.tiles;
-        const int tile0 = (int)(at - unit_start);
-        const int tile1 = (int)((end - unit_start < ln.tiles ? end - unit_start : ln.tiles));
-        const int row_tiles = (seq.nodes * G + kRows - 1) / kRows;
-        const int hk = (int)(unit / row_tiles), rt = (int)(unit % row_tiles);
-        const int rows = min(kRows, seq.nodes * G - rt * kRows);
+    Segment seg;
+    for (bool have = first_segment<kRows, kTile>(a, share, seg); have; have = next_segment<kRows, kTile>(a, share, seg)) {
+        const Seq& seq = seg.seq;
+        const int tile0 = seg.tile0, tile1 = seg.tile1;
+        const int hk = seg.hk, rt = seg.rt, rows = seg.rows;
         const int base = seq.len - seq.nodes;
 
         // ---- queries of rows r and r + 8, and what they see of the draft
@@ -297,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
             uint8_t* dst = ring + st * C::kStage;
             if (tile < tile1) {
                 // pages hold a multiple of 16 tokens: the whole step lies in one
-                int64_t row = pos < seq.len ? page_row(a.p, a.c, n, pos) : 0;
+                int64_t row = pos < seq.len ? page_row(a.p, a.c, seg.n, pos) : 0;
                 const bool bad = row < 0;
                 if (bad) {
                     if (lane == 0) set_status(a.status, kStatusBadSeqlens);
@@ -556,9 +402,8 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
             }
         }
         __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == ln.tiles;
-        const int slot = 2 * (int)blockIdx.x + (at == begin ? 0 : 1);
-        float* part = partials + slot * slot_floats(D);
+        const bool whole = tile0 == 0 && tile1 == seg.tiles;
+        float* part = partials + (2 * (int)blockIdx.x + seg.later) * slot_floats(D, a.slot_rows);
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), d = 4 * (x % (D / 4));
             float mt = kNegInf, lt = 0.f;
@@ -580,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
                 const int from = max(base, tile0 * kTile), to = min(seq.len, tile1 * kTile);
                 for (int p = from; p < to; ++p) {
                     if (!((bits >> (p - base)) & 1)) continue;
-                    const int64_t vr = page_row(a.p, a.c, n, p);
+                    const int64_t vr = page_row(a.p, a.c, seg.n, p);
                     if (vr < 0) continue;
                     const float4 z = load4(static_cast<const uint16_t*>(a.c.v) + (vr + head_rows) * D + d);
                     if (!(fabsf(z.x) <= FLT_MAX)) y.x += z.x;
@@ -592,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
             if (!whole) {
                 if (d == 0) {
                     part[row] = mt;
-                    part[kRows + row] = lt;
+                    part[a.slot_rows + row] = lt;
                 }
-                *reinterpret_cast<float4*>(part + 2 * kRows + row * D + d) = y;
+                *reinterpret_cast<float4*>(part + 2 * a.slot_rows + row * D + d) = y;
                 continue;
             }
             const float inv = mt == kNegInf && lt == 0.f ? 0.f : 1.f / lt;
@@ -609,13 +454,12 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
             if (a.lse && d == 0) a.lse[t * a.H + head] = mt == kNegInf && lt == 0.f ? kNegInf : mt * kLn2 + logf(lt);
         }
         __syncthreads();  // the rings are filled again
-        at = unit_start + tile1;
     }
 }
 
 // Joins the partials of the units that span CTAs: one warp per row.
-template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a, int grid) {
+template <int D, int ROWS, int TN>
+__global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int lane = threadIdx.x & 31;
     const int n = blockIdx.x / a.c.Hk, hk = blockIdx.x % a.c.Hk;
     const int G = a.H / a.c.Hk;
@@ -623,24 +467,20 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a, int grid) {
     pdl_wait_previous();
     const Seq seq = load_seq(a, n);
     if (x >= seq.nodes * G) return;
-    const int64_t* line = static_cast<const int64_t*>(a.workspace);
-    const int64_t total = line[a.p.N], shares = share_count(total, grid);
-    const Line ln = seq_line(a, seq);
-    const int row_tiles = (seq.nodes * G + kRows - 1) / kRows;
-    const int64_t start = line[n] + ((int64_t)hk * row_tiles + x / kRows) * ln.tiles;
-    const int64_t c0 = share_of(start, total, shares), c1 = share_of(start + ln.tiles - 1, total, shares);
+    const int rt = x / ROWS, row = x % ROWS;
+    const LineMeta line = line_meta(a)[rt];
+    const int64_t tiles = seq_tiles<TN>(seq);
+    const int64_t start = line_starts(a, rt)[n] + hk * tiles;
+    const int64_t c0 = share_of(start, line.total, line.shares);
+    const int64_t c1 = share_of(start + tiles - 1, line.total, line.shares);
     if (c0 == c1) return;  // one CTA had the whole unit and wrote it
-    const float* partials = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + line_bytes(a.p.N));
-    const int row = x % kRows;
-    auto part = [&](int64_t cta) {
-        const bool later = cta == c0 && share_start(c0, total, shares) != start;
-        return partials + (2 * cta + later) * slot_floats(D);
+    const float* partials = partial_base(a);
+    auto part = [&](int64_t c) {
+        const bool later = c == c0 && share_start(c0, line.total, line.shares) != start;
+        return partials + (2 * (line.first_cta + c) + later) * slot_floats(D, a.slot_rows);
     };
     float mt = kNegInf, lt = 0.f;
-    for (int64_t b = c0; b <= c1; b += 32) {
-        const float mi = b + lane <= c1 ? part(b + lane)[row] : kNegInf;
-        mt = fmaxf(mt, mi);
-    }
+    for (int64_t b = c0; b <= c1; b += 32) mt = fmaxf(mt, b + lane <= c1 ? part(b + lane)[row] : kNegInf);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
     constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4s of a lane
@@ -653,13 +493,13 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a, int grid) {
             const float* p = part(b + lane);
             const float mi = p[row];
             f = mi == kNegInf ? 1.f : exp2_approx(mi - mt);  // a part that saw nothing holds zeros (or NaN)
-            lt += p[kRows + row] * f;
+            lt += p[a.slot_rows + row] * f;
         }
         const int count = (int)(c1 - b + 1 < 32 ? c1 - b + 1 : 32);
 #pragma unroll 4
         for (int i = 0; i < count; ++i) {
             const float fi = __shfl_sync(0xffffffffu, f, i);
-            const float* p = part(b + i) + 2 * kRows + row * D;
+            const float* p = part(b + i) + 2 * a.slot_rows + row * D;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (4 * lane + 128 * v >= D) continue;
@@ -696,38 +536,66 @@ int sm_count() {
     return sms;
 }
 
-template <int D, bool E4M3>
-cudaError_t launch_config(const TreeArgs& a, cudaStream_t s) {
-    using C = Config<D, E4M3>;
-    const int grid = sm_count() * C::kCtas;
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    tree_kernel<D, E4M3><<<grid, kThreads, C::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int rows = a.max_nodes * (a.H / a.c.Hk);
-    return launch_pdl(join_kernel<D>, dim3(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps), dim3(kThreads), 0, s, a, grid);
-}
-
-template <int D>
-cudaError_t launch_dim(const TreeArgs& a, cudaStream_t s) {
-    return a.c.e4m3 ? launch_config<D, true>(a, s) : launch_config<D, false>(a, s);
-}
-
 template <int D>
 int ctas_dim(int e4m3) {
     return e4m3 ? Config<D, true>::kCtas : Config<D, false>::kCtas;
 }
 
+// The launch's shape from its sizes alone.
+struct Plan {
+    bool tc;  // the tcgen05 kernel
+    int grid, row_tiles, slot_rows, min_tiles;
+};
+Plan make_plan(int H, int Hk, int D, int max_nodes, int e4m3) {
+    Plan p;
+    const int rows = max_nodes * (H / Hk);
+    p.tc = rows > kRows;
+    const int tile = p.tc ? kTcRows : kRows;
+    p.row_tiles = (rows + tile - 1) / tile;
+    p.slot_rows = ((rows < tile ? rows : tile) + 3) / 4 * 4;
+    p.grid = sm_count() * (p.tc ? 1 : D == 64 ? ctas_dim<64>(e4m3) : D == 128 ? ctas_dim<128>(e4m3) : ctas_dim<256>(e4m3));
+    if (p.grid < p.row_tiles) p.grid = p.row_tiles;
+    p.min_tiles = p.tc ? 1 : 2;
+    return p;
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_config(const TreeArgs& a, bool tc, cudaStream_t s) {
+    using C = Config<D, E4M3>;
+    cudaError_t e;
+    const int rows = a.max_nodes * (a.H / a.c.Hk);
+    const dim3 join(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps);
+    if (tc) {
+        if ((e = launch_tree_tc(a, s)) != cudaSuccess) return e;
+        return launch_pdl(join_kernel<D, kTcRows, (D == 256 ? 64 : 128)>, join, dim3(kThreads), 0, s, a);
+    }
+    e = cudaFuncSetAttribute(tree_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    tree_kernel<D, E4M3><<<a.grid, kThreads, C::kSmem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_pdl(join_kernel<D, kRows, kTile>, join, dim3(kThreads), 0, s, a);
+}
+
+template <int D>
+cudaError_t launch_dim(const TreeArgs& a, bool tc, cudaStream_t s) {
+    return a.c.e4m3 ? launch_config<D, true>(a, tc, s) : launch_config<D, false>(a, tc, s);
+}
+
 }  // namespace
 
 size_t tree_workspace_bytes(int N, int H, int Hk, int D, int max_nodes, int e4m3) {
-    (void)H; (void)Hk; (void)max_nodes;
-    const int ctas = D == 64 ? ctas_dim<64>(e4m3) : D == 128 ? ctas_dim<128>(e4m3) : ctas_dim<256>(e4m3);
-    return line_bytes(N) + 2 * (size_t)sm_count() * ctas * slot_floats(D) * sizeof(float);
+    const Plan p = make_plan(H, Hk, D, max_nodes, e4m3);
+    return meta_bytes(p.row_tiles, N) + 2 * (size_t)p.grid * slot_floats(D, p.slot_rows) * sizeof(float);
 }
 
-cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
-    return a.c.D == 64 ? launch_dim<64>(a, s) : a.c.D == 128 ? launch_dim<128>(a, s) : launch_dim<256>(a, s);
+cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
+    TreeArgs a = args;
+    const Plan p = make_plan(a.H, a.c.Hk, a.c.D, a.max_nodes, a.c.e4m3);
+    a.grid = p.grid;
+    a.row_tiles = p.row_tiles;
+    a.slot_rows = p.slot_rows;
+    a.min_tiles = p.min_tiles;
+    return a.c.D == 64 ? launch_dim<64>(a, p.tc, s) : a.c.D == 128 ? launch_dim<128>(a, p.tc, s) : launch_dim<256>(a, p.tc, s);
 }
 
 }  // namespace gdn

@@ -1,0 +1,267 @@
+// Shared device code of the tree-attention kernels: the line of work, its
+// shares and segments, the workspace, and small helpers.
+//
+// Query rows of a (sequence, key/value head) -- (node, query head of the group)
+// pairs, node-major -- are cut into row tiles. The line of a row tile rt is the
+// token tiles of all (sequence, head) units that have it, sequences in order.
+// The grid is dealt to the row tiles in proportion to their lines, and each
+// CTA takes an equal stretch of its row tile's line; CTAs of different row
+// tiles with equal lines walk the same cache rows at the same time, so that
+// all but the first read them from L2. A stretch is walked in segments, one per
+// unit it touches. A unit within one CTA is finished there; one that spans CTAs
+// leaves a partial (m, l, o unnormalised) in each, which join_kernel adds up in
+// the CTAs' order: the result does not depend on timing.
+#pragma once
+
+#include "kv_page.cuh"
+
+namespace gdn {
+
+constexpr int kTcRows = 128;    // query rows of a row tile (tcgen05 kernel)
+constexpr int kMaxRowTiles = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// bf16x2 of the two e4m3 codes in the high bytes of x's halves: sign to sign,
+// the other seven bits four places down, which leaves the value times 2^-120
+// (subnormals included); the product with 2^120 is exact.
+__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t x) {
+    const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+    uint32_t z;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x7B807B80u));  // 2^120
+    return z;
+}
+
+// Asynchronous copies that write zeros where `on` is false (nothing is read).
+__device__ __forceinline__ void cp_async_zfill16(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = on ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_zfill8(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = on ? 8 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_zfill4(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = on ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sequence n's draft and length, checked; no nodes where there is nothing to do.
+struct Seq {
+    int first, nodes, len;  // first packed token, drafted tokens, cached tokens
+    bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const TreeArgs& a, int n) {
+    Seq q;
+    q.first = a.p.cu[n];
+    const int64_t end = a.p.cu[n + 1], nodes = end - q.first;
+    q.len = a.p.lens[n];
+    q.bad = q.first < 0 || nodes < 0 || end > a.T || nodes > a.max_nodes || q.len < nodes ||
+            q.len > ((int64_t)a.p.max_pages << a.c.page_shift);
+    q.nodes = q.bad ? 0 : (int)nodes;
+    return q;
+}
+
+// One row tile's line, in the workspace for the joining kernel.
+struct LineMeta {
+    int64_t total, shares, first_cta;
+};
+
+// Workspace: LineMeta [row_tiles]; the start of every sequence on every line,
+// int64 [row_tiles][N]; per CTA two partials (of the segment at the start of
+// its stretch, and of one that starts later), each m, l [slot_rows] and o
+// [slot_rows][D].
+__host__ __device__ inline size_t meta_bytes(int row_tiles, int N) {
+    return (sizeof(LineMeta) * row_tiles + (size_t)row_tiles * N * 8 + 255) / 256 * 256;
+}
+__host__ __device__ inline size_t slot_floats(int D, int slot_rows) { return (size_t)slot_rows * (D + 2); }
+
+__device__ __forceinline__ LineMeta* line_meta(const TreeArgs& a) { return static_cast<LineMeta*>(a.workspace); }
+__device__ __forceinline__ int64_t* line_starts(const TreeArgs& a, int rt) {
+    return reinterpret_cast<int64_t*>(line_meta(a) + a.row_tiles) + (int64_t)rt * a.p.N;
+}
+__device__ __forceinline__ float* partial_base(const TreeArgs& a) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + meta_bytes(a.row_tiles, a.p.N));
+}
+
+template <int ROWS>
+__device__ __forceinline__ int seq_row_tiles(const TreeArgs& a, const Seq& q) {
+    return (q.nodes * (a.H / a.c.Hk) + ROWS - 1) / ROWS;
+}
+template <int TN>
+__device__ __forceinline__ int64_t seq_tiles(const Seq& q) {
+    return (q.len + TN - 1) / TN;
+}
+
+// This CTA's stretch: tiles [begin, end) of row tile rt's line; `begin` lies in
+// sequence n, which starts at n_start.
+struct Share {
+    int64_t begin, end, n_start;
+    int rt, n;
+};
+
+__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t shares) { return c * total / shares; }
+__device__ __forceinline__ int64_t share_of(int64_t tile, int64_t total, int64_t shares) {
+    return ((tile + 1) * shares - 1) / total;  // the c with share_start(c) <= tile < share_start(c + 1)
+}
+
+// Every thread of the CTA takes part (it synchronises the CTA). The first CTA
+// of each row tile also writes that line's data to the workspace.
+template <int ROWS, int TN, int THREADS>
+__device__ __forceinline__ Share find_share(const TreeArgs& a) {
+    constexpr int W = THREADS / 32;
+    __shared__ unsigned long long totals[kMaxRowTiles];
+    __shared__ int64_t scan[W], found[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int N = a.p.N, RT = a.row_tiles;
+    if (tid < RT) totals[tid] = 0;
+    if (tid == 0) found[0] = N;
+    __syncthreads();
+    for (int n = tid; n < N; n += THREADS) {
+        const Seq q = load_seq(a, n);
+        if (q.bad && blockIdx.x == 0) set_status(a.status, kStatusBadSeqlens);
+        const int last = seq_row_tiles<ROWS>(a, q) - 1;
+        if (last >= 0) atomicAdd(&totals[last], (unsigned long long)(a.c.Hk * seq_tiles<TN>(q)));
+    }
+    __syncthreads();
+    // line rt holds every sequence with more than rt row tiles
+    int64_t all = 0, active = 0, run = 0;
+    for (int rt = RT - 1; rt >= 0; --rt) {
+        run += (int64_t)totals[rt];
+        all += run;
+        active += run > 0;
+    }
+    Share s;
+    s.begin = s.end = 0;
+    s.rt = RT;
+    s.n = N;
+    s.n_start = 0;
+    int64_t shares = 0, total = 0;
+    int cta = 0;
+    bool first_cta = false;
+    {
+        int64_t line = run;  // line 0
+        for (int rt = 0; rt < RT; ++rt) {
+            int64_t count = line > 0 ? 1 + ((int64_t)gridDim.x - active) * line / all : 0;
+            int64_t sh = line / a.min_tiles;
+            sh = sh < 1 ? 1 : sh < count ? sh : count;
+            if (line == 0) sh = 0;
+            if (blockIdx.x == 0 && tid == 0) line_meta(a)[rt] = LineMeta{line, sh, cta};
+            const bool here = blockIdx.x >= (unsigned)cta && blockIdx.x < (unsigned)(cta + count);
+            if (here) {
+                s.rt = rt;
+                shares = sh;
+                total = line;
+                first_cta = blockIdx.x == (unsigned)cta;
+                const int64_t c = blockIdx.x - cta;
+                if (c < sh) {
+                    s.begin = share_start(c, line, sh);
+                    s.end = share_start(c + 1, line, sh);
+                }
+            }
+            cta += (int)count;
+            line -= (int64_t)totals[rt];
+        }
+    }
+    (void)total;
+    (void)shares;
+    if (s.begin == s.end) return s;
+    int64_t before = 0;
+    for (int n0 = 0; n0 < N; n0 += THREADS) {
+        const int n = n0 + tid;
+        int64_t own = 0;
+        if (n < N) {
+            const Seq q = load_seq(a, n);
+            if (seq_row_tiles<ROWS>(a, q) > s.rt) own = a.c.Hk * seq_tiles<TN>(q);
+        }
+        int64_t x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int64_t pre = before;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) pre += scan[w];
+            before += scan[w];
+        }
+        const int64_t start = pre + x - own;
+        if (first_cta && n < N) line_starts(a, s.rt)[n] = start;
+        if (start <= s.begin && s.begin < start + own) {
+            found[0] = n;
+            found[1] = start;
+        }
+        __syncthreads();
+        if (!first_cta && found[0] < N) break;
+    }
+    s.n = (int)found[0];
+    s.n_start = found[1];
+    return s;
+}
+
+// The part of a CTA's stretch that lies in one unit.
+struct Segment {
+    Seq seq;
+    int n, hk, rt, rows;      // rows: query rows of this row tile
+    int tile0, tile1, tiles;  // its token tiles, of the unit's
+    int later;                // 0: it starts where the stretch starts
+    int64_t n_start, end;     // of the sequence and of this segment, on the line
+};
+
+template <int ROWS, int TN>
+__device__ __forceinline__ void place_segment(const TreeArgs& a, const Share& s, int64_t at, Segment& g) {
+    g.tiles = (int)seq_tiles<TN>(g.seq);
+    const int64_t unit = (at - g.n_start) / g.tiles, unit_start = g.n_start + unit * g.tiles;
+    g.hk = (int)unit;
+    g.tile0 = (int)(at - unit_start);
+    g.tile1 = (int)(s.end - unit_start < g.tiles ? s.end - unit_start : g.tiles);
+    g.later = at != s.begin;
+    g.rt = s.rt;
+    g.rows = min(ROWS, g.seq.nodes * (a.H / a.c.Hk) - s.rt * ROWS);
+    g.end = unit_start + g.tile1;
+}
+template <int ROWS, int TN>
+__device__ __forceinline__ bool first_segment(const TreeArgs& a, const Share& s, Segment& g) {
+    if (s.begin == s.end) return false;
+    g.n = s.n;
+    g.n_start = s.n_start;
+    g.seq = load_seq(a, g.n);
+    place_segment<ROWS, TN>(a, s, s.begin, g);
+    return true;
+}
+template <int ROWS, int TN>
+__device__ __forceinline__ bool next_segment(const TreeArgs& a, const Share& s, Segment& g) {
+    const int64_t at = g.end;
+    if (at >= s.end) return false;
+    int64_t len = a.c.Hk * seq_tiles<TN>(g.seq);
+    while (at >= g.n_start + len) {  // the next sequence on the line
+        g.n_start += len;
+        g.seq = load_seq(a, ++g.n);
+        len = seq_row_tiles<ROWS>(a, g.seq) > s.rt ? a.c.Hk * seq_tiles<TN>(g.seq) : 0;
+    }
+    place_segment<ROWS, TN>(a, s, at, g);
+    return true;
+}
+
+}  // namespace gdn

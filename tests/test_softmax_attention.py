@@ -414,14 +414,16 @@ ATTEND = [  # lens, counts, H, Hk, D, page
 @pytest.mark.parametrize("lens,counts,H,Hk,D,page", ATTEND)
 @pytest.mark.parametrize("held", [F8, BF])
 @pytest.mark.parametrize("form", ["chain", "tree"])
-def test_tree_attention(lens, counts, H, Hk, D, page, held, form):
+@pytest.mark.parametrize("most", ["tight", "loose"])  # max_nodes: the largest draft, or 64
+def test_tree_attention(lens, counts, H, Hk, D, page, held, form, most):
     pool = Pool(lens, counts, Hk, D, page, held, fill=31)
     T = sum(counts)
     wide = rnd(32, T, H * D + 8, dtype=BF, scale=1.5).to(DEV)
     q = wide[:, :H * D].unflatten(1, (H, D))
     mask = trees(counts, 5) if form == "tree" else None
     gate = rnd(33, T, H, D, dtype=BF).to(DEV) if form == "tree" else None
-    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=64, mask=None if mask is None else mask.to(DEV),
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=max(counts) if most == "tight" else 64,
+                                mask=None if mask is None else mask.to(DEV),
                                 gate=gate, return_lse=True)
     gdn.check_device_status(DEV)
     check_attention(pool, q, o, lse, mask, D ** -0.5, gate)

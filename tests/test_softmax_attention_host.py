@@ -134,7 +134,7 @@ def attend(L, **kw):
 
 @pytest.mark.parametrize("kw,expect", FROM_PAGES + [
     (dict(dt=0), UNSUPPORTED), (dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID),
-    (dict(H=3), INVALID), (dict(H=130), UNSUPPORTED), (dict(nodes=0), INVALID), (dict(nodes=65), UNSUPPORTED),
+    (dict(H=3), INVALID), (dict(H=130), UNSUPPORTED), (dict(cache=cache(n_pages=1 << 27)), UNSUPPORTED), (dict(nodes=0), INVALID), (dict(nodes=65), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(cache=cache(D=96)), UNSUPPORTED), (dict(q=None), INVALID),
     (dict(o=None), INVALID), (dict(o=A), INVALID), (dict(q=A + 8), INVALID), (dict(gate=A + 2), INVALID),
