@@ -9,24 +9,25 @@
 // with lse = -inf.
 //
 // Bound by reading the cache: 2 D bytes (e4m3; twice that in bf16) per cached
-// token and head, against 4 D flops per query row. Rows of one key/value head
-// (nodes x H / Hk) are taken 16 at a time as the M side of mma.sync m16n8k16,
-// so each cached element is converted once per 16 rows. A warp streams 16
-// tokens per step through a private ring in shared memory filled by
-// cp.async: each lane copies exactly the 16-byte pieces that it will use as
-// its fragments (the contraction order over d, and the column order of the
-// output, are free, so a lane's fragments are contiguous pieces of a row), and
-// the ring needs no barrier. The work -- 64-token tiles of all (sequence, kv
-// head, row tile) units in one line -- is cut into equal shares, one per CTA,
-// so that ragged lengths and few sequences load every SM alike; a unit that
-// spans CTAs leaves partial sums (m, l, o unnormalised, fp32) in the workspace,
-// which a second kernel joins.
+// token and head, against 4 D flops per query row.
 //
-// e4m3 values enter the products as bf16, exactly (a bit rearrangement times
-// 2^120); keys' scales multiply the scores and values' scales the
-// probabilities, both fp32. The probabilities are rounded to bf16 for the
-// second product (at most 2^-8 relative each, with errors that average out over
-// the sum); sums, maxima and outputs are fp32.
+// This file: up to 16 query rows of a key/value head (a decode step, a short
+// draft), where the cache streams through registers. Tokens are the M side of
+// mma.sync m16n8k16 and rows the N side, eight at a time, so that few rows
+// waste nothing: S^T = K Q^T and O^T = V^T P^T. A warp takes 16 tokens per step
+// from a private ring in shared memory that it fills with cp.async; nothing but
+// the end of a segment synchronises the CTA. The order of the contraction over
+// d and of the output's d is free: a lane's fragments are whole 16-byte pieces
+// of a row, whatever elements those are. More rows: tree_attn_tc.cu.
+//
+// e4m3 values enter the products as f16, exactly, by the hardware conversion
+// (one instruction for two; through bf16 it would take five), and so do the
+// queries, each row scaled by a power of two into f16's range. Keys' scales
+// multiply the scores in fp32. Values' scales multiply the probabilities; the
+// running reference R of a row is over s_j + log2 vs_j, so that the largest
+// weight e^{s - R} vs is about one and f16 (11 bits) holds the others next to
+// it, however the scales differ. R moves, and the sums are rescaled, only when
+// a weight would pass 2^8. Sums, maxima and outputs are fp32.
 #include <cfloat>
 #include <climits>
 
@@ -38,299 +39,350 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kRows = 16;           // query rows of a unit
+constexpr int kRows = 16;           // most query rows of a unit
 constexpr int kTile = 16 * kWarps;  // tokens of a tile: 16 per warp
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-template <int D, bool E4M3>
+// Transpose of an 8 x 8 matrix of 16-bit values, one row's pair per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, bool E4M3, int NT>
 struct Config {
-    static constexpr int kElem = E4M3 ? 1 : 2;
-    static constexpr int kRowBytes = D * kElem;
-    static constexpr int kKChunks = kRowBytes / 64;                     // 16-byte pieces of a key row per lane (4 lanes)
-    static constexpr int kVBytes = kRowBytes / 8 < 16 ? kRowBytes / 8 : 16;  // piece of a value row (8 lanes)
-    static constexpr int kVChunks = kRowBytes / 8 / kVBytes;
-    static constexpr int kVElems = kVBytes / kElem;
-    static constexpr int kKStage = 2 * kKChunks * 512;                  // 16 tokens of one warp
-    static constexpr int kVStage = 4 * kVChunks * kVBytes * 32;
-    static constexpr int kScales = E4M3 ? 128 : 0;                      // k then v scales of 16 tokens
-    static constexpr int kStage = kKStage + kVStage + kScales;
-    // stages: about 8 KB per warp and stage at two or three CTAs per SM fill the
-    // SM's share of bandwidth times latency several times over
-    static constexpr int kStages = kStage > 8000 ? 3 : 4;
-    static constexpr int kRing = kStages * kStage * kWarps;
-    static constexpr int kMerge = kWarps * kRows * D * 4 + kWarps * kRows * 8;
-    static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + (D == 256 ? D / 16 * 512 : 0);
-    static constexpr int kCtas = kSmem > 113 * 1024 ? 1 : kSmem > 75 * 1024 ? 2 : 3;
+    static constexpr int kRowBytes = E4M3 ? D : 2 * D;
+    static constexpr int kChunks = kRowBytes / 16;  // 16-byte pieces of a row
+    static constexpr int kSide = 16 * kRowBytes;    // keys (or values) of a step
+    static constexpr int kStage = 2 * kSide + (E4M3 ? 128 : 0);
+    // Q fragments stay in registers while they and the output leave room
+    static constexpr bool kQInSmem = NT * D > 256;
+    static constexpr int kQBytes = kQInSmem ? NT * D / 16 * 256 : 0;
+    static constexpr int kMerge = kWarps * 8 * NT * (D + 2) * 4;
+    static constexpr int ring(int stages) { return stages * kStage * kWarps; }
+    static constexpr int smem(int stages) { return (ring(stages) > kMerge ? ring(stages) : kMerge) + kQBytes; }
+    static constexpr bool fits(int ctas, int stages) { return ctas * (smem(stages) + 1536) <= 227 * 1024; }
+    // CTAs per SM: what the registers of the output allow, then what a ring of
+    // two stages (the one in use and one in flight) allows; then stages
+    static constexpr int kWant = NT * D <= 128 ? 4 : NT * D <= 256 ? 3 : 2;
+    static constexpr int kCtas = fits(kWant, 2) ? kWant : fits(kWant - 1, 2) ? kWant - 1 : 1;
+    static constexpr int kStages = fits(kCtas, 4) ? 4 : fits(kCtas, 3) ? 3 : 2;
+    static constexpr int kSmem = smem(kStages);
+
+    // Row of token label x (0..7) of a step's half, and the 16-byte piece that
+    // lane row r takes of a value row's 128 bytes: eight lanes of a shared-memory
+    // access then meet eight different bank groups under the swizzle below.
+    static __device__ __forceinline__ int token(int x) { return kRowBytes >= 128 ? ((x & 1) << 2) | (x >> 1) : x; }
+    static __device__ __forceinline__ int piece(int r) { return kRowBytes >= 128 ? ((r & 1) << 2) | (r >> 1) : r; }
+    static __device__ __forceinline__ int offset(int row, int chunk) {
+        const int swz = kRowBytes >= 128 ? row & 7 : (row >> 1) & 3;
+        return row * kRowBytes + ((chunk ^ swz) << 4);
+    }
 };
 
-// The fragments' element order: k-step ks of the first product takes, from
-// lane column c, elements dk .. dk + 3 of the row; word 0 of the fragment pair
-// holds elements {0, 2} (e4m3: even bytes) or {0, 1} (bf16), word 1 the others.
+// First of the four elements that lane column c holds for k-step ks of the
+// first product (its two fragment words take two each).
 template <bool E4M3>
 __device__ __forceinline__ int k_elem(int ks, int c) {
     return E4M3 ? 64 * (ks >> 2) + 16 * c + 4 * (ks & 3) : 32 * (ks >> 1) + 8 * c + 4 * (ks & 1);
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kernel(TreeArgs a) {
-    using C = Config<D, E4M3>;
-    constexpr int kSteps = D / 16;
-    constexpr bool kQInSmem = D == 256;
+// NT: groups of eight query rows.
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_kernel(TreeArgs a) {
+    using C = Config<D, E4M3, NT>;
+    constexpr int kSteps = D / 16, RB = C::kRowBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
     const int G = a.H / a.c.Hk;
     pdl_launch_dependents();
-
     const Share share = find_share<kRows, kTile, kThreads>(a);
 
     float* partials = partial_base(a);
     uint8_t* ring = smem + warp * C::kStages * C::kStage;
-    uint32_t* q_smem = reinterpret_cast<uint32_t*>(smem + C::kSmem - (kQInSmem ? kSteps * 512 : 0));
+    uint32_t* q_smem = reinterpret_cast<uint32_t*>(smem + C::kSmem - C::kQBytes);
 
     Segment seg;
     for (bool have = first_segment<kRows, kTile>(a, share, seg); have; have = next_segment<kRows, kTile>(a, share, seg)) {
         const Seq& seq = seg.seq;
         const int tile0 = seg.tile0, tile1 = seg.tile1;
-        const int hk = seg.hk, rt = seg.rt, rows = seg.rows;
+        const int hk = seg.hk, rows = seg.rows;
         const int base = seq.len - seq.nodes;
-
-        // ---- queries of rows r and r + 8, and what they see of the draft
-        uint32_t qf[kQInSmem ? 1 : kSteps][4];
-        uint64_t sees[2];
-        const uint16_t* qp[2];
-        bool live[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = r + 8 * i;
-            live[i] = row < rows;
-            const int node = live[i] ? (rt * kRows + row) / G : 0;
-            const int head = live[i] ? hk * G + (rt * kRows + row) % G : 0;
-            const int64_t t = seq.first + node;
-            qp[i] = static_cast<const uint16_t*>(a.q) + t * a.ld_q + (int64_t)head * D;
-            sees[i] = !live[i] ? 0 : a.mask ? (uint64_t)a.mask[t] : (2ull << node) - 1;
-        }
-        auto q_words = [&](int ks, uint32_t (&w)[4]) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint2 x = make_uint2(0, 0);
-                if (live[i]) x = *reinterpret_cast<const uint2*>(qp[i] + k_elem<E4M3>(ks, c));
-                w[i] = E4M3 ? __byte_perm(x.x, x.y, 0x5410) : x.x;      // elements 0, 2 | 0, 1
-                w[2 + i] = E4M3 ? __byte_perm(x.x, x.y, 0x7632) : x.y;  // elements 1, 3 | 2, 3
-            }
-        };
-        if (kQInSmem) {
-            for (int ks = warp; ks < kSteps; ks += kWarps) {
-                uint32_t w[4];
-                q_words(ks, w);
-                *reinterpret_cast<uint4*>(q_smem + (ks * 32 + lane) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            __syncthreads();
-        } else {
-#pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) q_words(ks, qf[ks]);
-        }
-
-        // ---- the ring: this warp's 16 tokens of tile `tile` into stage `st`
         const int64_t head_rows = (int64_t)hk << a.c.page_shift;
-        auto issue = [&](int tile, int st) {
+
+        // ---- the ring: this warp's 16 tokens of a tile into stage st. Pages hold a
+        // multiple of 16 tokens: a step lies in one, its rows back to back.
+        auto page_of = [&](int tile) -> int64_t {  // row of the step's first token; -1: nothing there
             const int pos = tile * kTile + warp * 16;
+            if (tile >= tile1 || pos >= seq.len) return -1;
+            const int64_t row = page_row(a.p, a.c, seg.n, pos);
+            if (row < 0 && lane == 0) set_status(a.status, kStatusBadSeqlens);
+            return row < 0 ? -1 : row + head_rows;
+        };
+        auto issue = [&](int tile, int64_t row, int st) {
             uint8_t* dst = ring + st * C::kStage;
+            const int left = row < 0 ? 0 : seq.len - (tile * kTile + warp * 16);  // tokens that exist
             if (tile < tile1) {
-                // pages hold a multiple of 16 tokens: the whole step lies in one
-                int64_t row = pos < seq.len ? page_row(a.p, a.c, seg.n, pos) : 0;
-                const bool bad = row < 0;
-                if (bad) {
-                    if (lane == 0) set_status(a.status, kStatusBadSeqlens);
-                    row = 0;
-                }
-                const int left = bad ? 0 : seq.len - pos;  // tokens of the step that exist
-                row += bad || left <= 0 ? 0 : head_rows;
-                const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + row * C::kRowBytes;
-                const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + row * C::kRowBytes;
+                const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + (row < 0 ? 0 : row) * RB + 16 * lane;
+                const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + (row < 0 ? 0 : row) * RB + 16 * lane;
+                if (left >= 16) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int tok = 8 * nt + r;
-                    const bool on = tok < left;
+                    for (int i = 0; i < C::kSide / 512; ++i) {
+                        const int p = lane + 32 * i;
+                        cp_async_16(dst + C::offset(p / C::kChunks, p % C::kChunks), kb + 512 * i);
+                    }
 #pragma unroll
-                    for (int j = 0; j < C::kKChunks; ++j)
-                        cp_async_zfill16(dst + ((nt * C::kKChunks + j) * 32 + lane) * 16,
-                                         kb + (on ? tok : 0) * C::kRowBytes + 64 * j + 16 * c, on);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int tok = 2 * c + (x & 1) + 8 * (x >> 1);
-                    const bool on = tok < left;
-#pragma unroll
-                    for (int j = 0; j < C::kVChunks; ++j) {
-                        uint8_t* d = dst + C::kKStage + ((x * C::kVChunks + j) * 32 + lane) * C::kVBytes;
-                        const uint8_t* s = vb + (on ? tok : 0) * C::kRowBytes + (8 * j + r) * C::kVBytes;
-                        if (C::kVBytes == 16) cp_async_zfill16(d, s, on);
-                        else cp_async_zfill8(d, s, on);
+                    for (int i = 0; i < C::kSide / 512; ++i) {
+                        const int p = lane + 32 * i;
+                        cp_async_16(dst + C::kSide + C::offset(p / C::kChunks, p % C::kChunks), vb + 512 * i);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < C::kSide / 512; ++i) {
+                        const int p = lane + 32 * i, tok = p / C::kChunks;
+                        const bool on = tok < left;
+                        cp_async_zfill16(dst + C::offset(tok, p % C::kChunks), on ? kb + 512 * i : kb, on);
+                        cp_async_zfill16(dst + C::kSide + C::offset(tok, p % C::kChunks), on ? vb + 512 * i : vb, on);
                     }
                 }
                 if (E4M3) {
-                    const int tok = lane & 15;
-                    const float* s = (lane < 16 ? a.c.k_scale : a.c.v_scale) + row + (tok < left ? tok : 0);
-                    cp_async_zfill4(dst + C::kKStage + C::kVStage + 4 * lane, s, tok < left);
+                    const float* s = (lane < 16 ? a.c.k_scale : a.c.v_scale) + (row < 0 ? 0 : row);
+                    const bool on = (lane & 15) < left;
+                    cp_async_zfill4(dst + 2 * C::kSide + 4 * lane, s + (on ? lane & 15 : 0), on);
                 }
             }
             cp_async_commit_group();
         };
+        int64_t next_row;
+#pragma unroll
+        for (int st = 0; st < C::kStages - 1; ++st) issue(tile0 + st, page_of(tile0 + st), st);
+        next_row = page_of(tile0 + C::kStages - 1);
 
-        float o[D / 8][4];
+        // ---- queries: row 8 g + r as this lane's fragment column; what rows
+        // 8 g + 2 c + {0, 1} (this lane's scores) see of the draft
+        uint32_t qf[C::kQInSmem ? 1 : NT][C::kQInSmem ? 1 : kSteps][2];
+        float mul[NT][2], ref[NT][2], l[NT][2];
+        uint64_t sees[NT][2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int g = 0; g < NT; ++g) {
+            const bool live = 8 * g + r < rows;
+            const int64_t t = seq.first + (live ? 8 * g + r : 0) / G;
+            const uint16_t* qp = static_cast<const uint16_t*>(a.q) + t * a.ld_q + (int64_t)(hk * G + (live ? 8 * g + r : 0) % G) * D;
+            float down = 1.f, up = 1.f;  // the row's power of two, so that its largest element is in [1, 2)
+            if (E4M3) {
+                uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+                for (int ks = 0; ks < kSteps; ++ks) {
+                    const uint2 x = live ? *reinterpret_cast<const uint2*>(qp + k_elem<E4M3>(ks, c)) : make_uint2(0, 0);
+                    const uint32_t w[4] = {x.x & 0x7FFFu, x.x >> 16 & 0x7FFFu, x.y & 0x7FFFu, x.y >> 16 & 0x7FFFu};
+                    m = max(m, max(max(w[0], w[1]), max(w[2], w[3])));
+                }
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                uint32_t e = m >> 7;  // 127 + exponent; a row that is not finite stays as it is
+                e = e == 255u || m == 0u ? 127u : e < 1u ? 1u : e > 253u ? 253u : e;
+                down = __uint_as_float((254u - e) << 23);
+                up = __uint_as_float(e << 23);
+            }
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                const uint2 x = live ? *reinterpret_cast<const uint2*>(qp + k_elem<E4M3>(ks, c)) : make_uint2(0, 0);
+                uint32_t w[2] = {x.x, x.y};
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        w[i] = pack_f16(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
+                }
+                if (C::kQInSmem) {
+                    if (ks % kWarps == warp)
+                        *reinterpret_cast<uint2*>(q_smem + ((g * kSteps + ks) * 32 + lane) * 2) = make_uint2(w[0], w[1]);
+                } else {
+                    qf[C::kQInSmem ? 0 : g][C::kQInSmem ? 0 : ks][0] = w[0];
+                    qf[C::kQInSmem ? 0 : g][C::kQInSmem ? 0 : ks][1] = w[1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 8 * g + 2 * c + i;
+                mul[g][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * c + i)) * a.scale * kLog2e;
+                const bool on = row < rows;
+                const int node = on ? row / G : 0;
+                sees[g][i] = !on ? 0 : a.mask ? (uint64_t)a.mask[seq.first + node] : (2ull << node) - 1;
+                // a row that is not there: a reference that no score reaches and beside which all vanish
+                ref[g][i] = on ? kNegInf : 1e30f;
+                l[g][i] = 0.f;
+            }
+        }
+        if (C::kQInSmem) __syncthreads();
+
+        float o[D / 16][NT][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int g = 0; g < NT; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][g][e] = 0.f;
         bool odd = false;  // a drafted value was not finite
-        const float scale2 = a.scale * kLog2e;
 
-#pragma unroll
-        for (int st = 0; st < C::kStages - 1; ++st) issue(tile0 + st, st);
         int st = 0;
         for (int tile = tile0; tile < tile1; ++tile) {
             {
                 int next = st + C::kStages - 1;
                 if (next >= C::kStages) next -= C::kStages;
-                __syncwarp();  // every lane has read the stage (its scales) that is filled next
-                issue(tile + C::kStages - 1, next);
+                __syncwarp();  // every lane has read the stage that is filled next
+                issue(tile + C::kStages - 1, next_row, next);
+                next_row = page_of(tile + C::kStages);
             }
             cp_async_wait_group<C::kStages - 1>();
-            if (E4M3) __syncwarp();  // the scales were copied by other lanes
+            __syncwarp();  // the other lanes' copies as well
             const uint8_t* src = ring + st * C::kStage;
             if (++st == C::kStages) st = 0;
             const int pos = tile * kTile + warp * 16;
             if (pos >= seq.len) continue;
 
-            // ---- scores: rows r, r + 8 x tokens 8 nt + 2c, + 1
-            float s[2][4];
+            // ---- scores: tokens label r of either half x rows 2c, 2c + 1
+            float s[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int g = 0; g < NT; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-            }
+                for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < C::kKChunks; ++j) {
+            for (int j = 0; j < RB / 64; ++j) {
                 uint4 kw[2];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-                    kw[nt] = *reinterpret_cast<const uint4*>(src + ((nt * C::kKChunks + j) * 32 + lane) * 16);
+                for (int h = 0; h < 2; ++h)
+                    kw[h] = *reinterpret_cast<const uint4*>(src + C::offset(8 * h + C::token(r), 4 * j + c));
                 constexpr int per = E4M3 ? 4 : 2;  // k-steps of a 16-byte piece
 #pragma unroll
                 for (int x = 0; x < per; ++x) {
-                    uint32_t qa[4];
-                    if (kQInSmem) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(q_smem + ((per * j + x) * 32 + lane) * 4);
-                        qa[0] = u.x; qa[1] = u.y; qa[2] = u.z; qa[3] = u.w;
-                    } else {
+                    uint32_t ka[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) qa[e] = qf[kQInSmem ? 0 : per * j + x][e];
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const uint32_t w[4] = {kw[nt].x, kw[nt].y, kw[nt].z, kw[nt].w};
-                        uint32_t b0, b1;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w[4] = {kw[h].x, kw[h].y, kw[h].z, kw[h].w};
                         if (E4M3) {
-                            b0 = e4m3_hi_to_bf16x2(w[x] << 8);  // bytes 0, 2
-                            b1 = e4m3_hi_to_bf16x2(w[x]);       // bytes 1, 3
+                            ka[h] = e4m3x2_to_f16x2(w[x]);
+                            ka[2 + h] = e4m3x2_to_f16x2(w[x] >> 16);
                         } else {
-                            b0 = w[2 * x];
-                            b1 = w[2 * x + 1];
+                            ka[h] = w[(2 * x) & 3];
+                            ka[2 + h] = w[(2 * x + 1) & 3];
                         }
-                        mma_16816(s[nt], qa, b0, b1);
+                    }
+#pragma unroll
+                    for (int g = 0; g < NT; ++g) {
+                        uint32_t qb[2];
+                        if (C::kQInSmem) {
+                            const uint2 u = *reinterpret_cast<const uint2*>(q_smem + ((g * kSteps + per * j + x) * 32 + lane) * 2);
+                            qb[0] = u.x;
+                            qb[1] = u.y;
+                        } else {
+                            qb[0] = qf[C::kQInSmem ? 0 : g][C::kQInSmem ? 0 : per * j + x][0];
+                            qb[1] = qf[C::kQInSmem ? 0 : g][C::kQInSmem ? 0 : per * j + x][1];
+                        }
+                        mma_16816<E4M3>(s[g], ka, qb);
                     }
                 }
             }
-            // ---- softmax in powers of two
-            float vs[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+            // ---- softmax in powers of two; lv: log2 of the values' scales
+            float vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+            float ks[2] = {1.f, 1.f};
+            if (E4M3) {
+                const float* sc = reinterpret_cast<const float*>(src + 2 * C::kSide);
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                float2 k2 = make_float2(scale2, scale2);
-                if (E4M3) {
-                    const float* sc = reinterpret_cast<const float*>(src + C::kKStage + C::kVStage);
-                    const float2 x = *reinterpret_cast<const float2*>(sc + 8 * nt + 2 * c);
-                    const float2 y = *reinterpret_cast<const float2*>(sc + 16 + 8 * nt + 2 * c);
-                    k2 = make_float2(x.x * scale2, x.y * scale2);
-                    vs[nt][0] = y.x;
-                    vs[nt][1] = y.y;
+                for (int h = 0; h < 2; ++h) {
+                    ks[h] = sc[8 * h + C::token(r)];
+                    vs[h] = sc[16 + 8 * h + C::token(r)];
+                    lv[h] = log2_scale(vs[h]);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] *= e & 1 ? k2.y : k2.x;
             }
+#pragma unroll
+            for (int g = 0; g < NT; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[g][e] *= E4M3 ? mul[g][e & 1] * ks[e >> 1] : mul[g][e & 1];
             const bool drafted = pos + 16 > base;  // some token is not every row's
-            uint32_t on = 0xFFu;                   // bit nt * 4 + e
+            uint32_t on = ~0u;                     // bit 4 g + e
             if (drafted) {
                 on = 0;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int g = 0; g < NT; ++g)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int t = pos + 8 * nt + 2 * c + (e & 1);
-                        const bool see = t < base || (t < seq.len && ((sees[e >> 1] >> (t - base)) & 1));
-                        if (see) on |= 1u << (nt * 4 + e);
-                        else s[nt][e] = kNegInf;
+                        const int t = pos + 8 * (e >> 1) + C::token(r);
+                        const bool see = t < base || (t < seq.len && ((sees[g][e & 1] >> (t - base)) & 1));
+                        if (see) on |= 1u << (4 * g + e);
+                        else s[g][e] = kNegInf;
                     }
             }
-            float top[2];
+            bool grown = false;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                top[i] = fmaxf(m[i], x);
+            for (int g = 0; g < NT; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) grown = grown || s[g][e] + lv[e >> 1] > ref[g][e & 1] + kLazy;
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int g = 0; g < NT; ++g)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float top = fmaxf(s[g][i] + lv[0], s[g][2 + i] + lv[1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float old = ref[g][i];
+                        if (!(top > old)) continue;
+                        ref[g][i] = top;
+                        const float f = old == kNegInf ? 1.f : exp2_approx(old - top);  // nothing but zeros (or NaN) before
+                        l[g][i] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            o[j][g][i] *= f;
+                            o[j][g][2 + i] *= f;
+                        }
+                    }
             }
-            if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-                float f[2];
+            uint32_t pb[NT][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f[i] = m[i] == kNegInf ? 0.f : exp2_approx(m[i] - top[i]);
-                    l[i] *= f[i];
-                    m[i] = top[i];
-                }
+            for (int g = 0; g < NT; ++g)
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][0] *= f[0];
-                    o[i][1] *= f[0];
-                    o[i][2] *= f[1];
-                    o[i][3] *= f[1];
-                }
-            }
-            uint32_t pa[4];
+                for (int h = 0; h < 2; ++h) {
+                    float w[2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float ref = m[i] == kNegInf ? 0.f : m[i];
-                    float p[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        p[e] = exp2_approx(s[nt][2 * i + e] - ref);
-                        l[i] += p[e];
+                    for (int i = 0; i < 2; ++i) {
+                        const float p = exp2_approx(s[g][2 * h + i] - (ref[g][i] == kNegInf ? 0.f : ref[g][i]));
+                        l[g][i] += p;
                         // a token that the row does not see adds nothing, whatever its scale
-                        if (E4M3) p[e] = (on >> (nt * 4 + 2 * i + e)) & 1 ? p[e] * vs[nt][e] : 0.f;
+                        w[i] = !E4M3 ? p : (on >> (4 * g + 2 * h + i)) & 1 ? p * vs[h] : 0.f;
                     }
-                    pa[2 * nt + i] = pack_bf16(p[0], p[1]);
+                    pb[g][h] = transpose8(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
                 }
-            // ---- outputs: tokens {2c, 2c + 1, 2c + 8, 2c + 9} x this lane's piece of d
+            // ---- outputs: this lane's pieces of d x tokens labels 2c, 2c + 1 of either half
+            const uint8_t* vsrc = src + C::kSide;
+            constexpr int W = RB == 64 ? 2 : 4;   // words of a piece
+            constexpr int kPieces = RB / 32 / W;  // pieces of a lane
 #pragma unroll
-            for (int j = 0; j < C::kVChunks; ++j) {
-                constexpr int W = C::kVBytes / 4;
-                uint32_t v[4][W];
+            for (int j = 0; j < kPieces; ++j) {
+                uint32_t v[4][W];  // [half * 2 + token][word]
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint8_t* p = src + C::kKStage + ((x * C::kVChunks + j) * 32 + lane) * C::kVBytes;
+                    const int row = 8 * (x >> 1) + C::token(2 * c + (x & 1));
                     if (W == 4) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(p);
+                        const uint4 u = *reinterpret_cast<const uint4*>(vsrc + C::offset(row, 8 * j + C::piece(r)));
                         v[x][0] = u.x; v[x][1] = u.y; v[x][W > 2 ? 2 : 0] = u.z; v[x][W > 3 ? 3 : 1] = u.w;
                     } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(p);
+                        const uint2 u = *reinterpret_cast<const uint2*>(vsrc + C::offset(row, r >> 1) + 8 * (r & 1));
                         v[x][0] = u.x; v[x][1] = u.y;
                     }
                 }
@@ -340,67 +392,67 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            if ((v[x][w] & 0x7F80u) == 0x7F80u) v[x][w] &= 0xFFFF0000u, odd = true;
-                            if ((v[x][w] & 0x7F800000u) == 0x7F800000u) v[x][w] &= 0x0000FFFFu, odd = true;
-                        }
+                        for (int w = 0; w < W; ++w) odd |= zero_non_finite(v[x][w]);
                 }
-                constexpr int per = E4M3 ? 4 : 2;  // elements of a word
 #pragma unroll
-                for (int w = 0; w < W; ++w)
+                for (int w = 0; w < W; ++w) {
+                    if (E4M3) {
 #pragma unroll
-                    for (int e = 0; e < per; ++e) {
-                        uint32_t b0, b1;
-                        if (E4M3) {
-                            const uint32_t sel = 0x4000u + (uint32_t)e * 0x1111u;  // byte 1: v0's, byte 3: v1's
-                            b0 = e4m3_hi_to_bf16x2(__byte_perm(v[0][w], v[1][w], sel));
-                            b1 = e4m3_hi_to_bf16x2(__byte_perm(v[2][w], v[3][w], sel));
-                        } else {
-                            b0 = __byte_perm(v[0][w], v[1][w], e ? 0x7632 : 0x5410);
-                            b1 = __byte_perm(v[2][w], v[3][w], e ? 0x7632 : 0x5410);
+                        for (int y = 0; y < 2; ++y) {  // elements 4 w + 2 y, + 1 of the piece
+                            const uint32_t sel = y ? 0x7362 : 0x5140;
+                            const uint32_t h0 = __byte_perm(v[0][w], v[1][w], sel), h1 = __byte_perm(v[2][w], v[3][w], sel);
+                            const uint32_t va[4] = {e4m3x2_to_f16x2(h0), e4m3x2_to_f16x2(h0 >> 16), e4m3x2_to_f16x2(h1),
+                                                    e4m3x2_to_f16x2(h1 >> 16)};
+#pragma unroll
+                            for (int g = 0; g < NT; ++g) mma_16816<true>(o[(j * W + w) * 2 + y][g], va, pb[g]);
                         }
-                        mma_16816(o[j * C::kVElems + w * per + e], pa, b0, b1);
+                    } else {
+                        const uint32_t va[4] = {__byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[0][w], v[1][w], 0x7632),
+                                                __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632)};
+#pragma unroll
+                        for (int g = 0; g < NT; ++g) mma_16816<false>(o[(j * W + w) % (D / 16)][g], va, pb[g]);
                     }
+                }
             }
         }
         cp_async_wait_group<0>();
 
-        // ---- join the four warps: m, l and o of every row
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
+        // ---- join the four warps: reference, l and o of every row
         const bool any_odd = __syncthreads_or(odd);  // and the rings are drained: they hold the sums now
-        float* buf = reinterpret_cast<float*>(smem);                  // [warp][row][D]
-        float* mw = buf + kWarps * kRows * D;                         // [warp][row]
-        float* lw = mw + kWarps * kRows;
-        if (c == 0) {
+        float* buf = reinterpret_cast<float*>(smem);  // [warp][row][D]
+        float* mw = buf + kWarps * 8 * NT * D;        // [warp][row]
+        float* lw = mw + kWarps * 8 * NT;
+#pragma unroll
+        for (int g = 0; g < NT; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mw[warp * kRows + r + 8 * i] = m[i];
-                lw[warp * kRows + r + 8 * i] = l[i];
+                l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], 4);
+                l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], 8);
+                l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], 16);
+                if (r == 0) {
+                    mw[warp * 8 * NT + 8 * g + 2 * c + i] = ref[g][i];
+                    lw[warp * 8 * NT + 8 * g + 2 * c + i] = l[g][i];
+                }
             }
-        }
         __syncthreads();
-        float top[2], f[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            top[i] = kNegInf;
+        for (int g = 0; g < NT; ++g)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top[i] = fmaxf(top[i], mw[w * kRows + r + 8 * i]);
-            f[i] = m[i] == kNegInf ? 0.f : exp2_approx(m[i] - top[i]);
-        }
+            for (int i = 0; i < 2; ++i) {
+                const int row = 8 * g + 2 * c + i;
+                float top = kNegInf;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            // column 2c + e of tile j: lane r = 2c + e of the value fragments, element j of its pieces
-            const int piece = j / C::kVElems, x = j % C::kVElems;
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mw[w * 8 * NT + row]);
+                const float f = ref[g][i] == kNegInf ? 1.f : exp2_approx(ref[g][i] - top);
+                constexpr int kElems = RB == 64 ? 8 : E4M3 ? 16 : 8;  // of a piece
+                float* y = buf + (warp * 8 * NT + row) * D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = (8 * piece + 2 * c + (e & 1)) * C::kVElems + x;
-                buf[(warp * kRows + r + 8 * (e >> 1)) * D + d] = o[j][e] * f[e >> 1];
+                for (int j = 0; j < D / 16; ++j) {
+                    // output tile j: elements 2 j', 2 j' + 1 of the lane's piece j * 2 / kElems
+                    const int d = (8 * (2 * j / kElems) + C::piece(r)) * kElems + 2 * j % kElems;
+                    *reinterpret_cast<float2*>(y + d) = make_float2(o[j][g][i] * f, o[j][g][2 + i] * f);
+                }
             }
-        }
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == seg.tiles;
         float* part = partials + (2 * (int)blockIdx.x + seg.later) * slot_floats(D, a.slot_rows);
@@ -408,16 +460,16 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3>::kCtas)) tree_kerne
             const int row = x / (D / 4), d = 4 * (x % (D / 4));
             float mt = kNegInf, lt = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, mw[w * kRows + row]);
+            for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, mw[w * 8 * NT + row]);
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw_ = mw[w * kRows + row];
-                lt += mw_ == kNegInf ? lw[w * kRows + row] : lw[w * kRows + row] * exp2_approx(mw_ - mt);
-                const float4 z = *reinterpret_cast<const float4*>(buf + (w * kRows + row) * D + d);
+                const float m = mw[w * 8 * NT + row];
+                lt += m == kNegInf ? lw[w * 8 * NT + row] : lw[w * 8 * NT + row] * exp2_approx(m - mt);
+                const float4 z = *reinterpret_cast<const float4*>(buf + (w * 8 * NT + row) * D + d);
                 y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
             }
-            const int node = (rt * kRows + row) / G, head = hk * G + (rt * kRows + row) % G;
+            const int node = row / G, head = hk * G + row % G;
             const int64_t t = seq.first + node;
             if (!E4M3 && any_odd) {
                 // drafted values that are not finite, for the rows that see them
@@ -537,8 +589,9 @@ int sm_count() {
 }
 
 template <int D>
-int ctas_dim(int e4m3) {
-    return e4m3 ? Config<D, true>::kCtas : Config<D, false>::kCtas;
+int ctas_dim(int e4m3, int rows) {
+    if (rows <= 8) return e4m3 ? Config<D, true, 1>::kCtas : Config<D, false, 1>::kCtas;
+    return e4m3 ? Config<D, true, 2>::kCtas : Config<D, false, 2>::kCtas;
 }
 
 // The launch's shape from its sizes alone.
@@ -553,26 +606,29 @@ Plan make_plan(int H, int Hk, int D, int max_nodes, int e4m3) {
     const int tile = p.tc ? kTcRows : kRows;
     p.row_tiles = (rows + tile - 1) / tile;
     p.slot_rows = ((rows < tile ? rows : tile) + 3) / 4 * 4;
-    p.grid = sm_count() * (p.tc ? 1 : D == 64 ? ctas_dim<64>(e4m3) : D == 128 ? ctas_dim<128>(e4m3) : ctas_dim<256>(e4m3));
+    p.grid = sm_count();
+    if (!p.tc) p.grid *= D == 64 ? ctas_dim<64>(e4m3, rows) : D == 128 ? ctas_dim<128>(e4m3, rows) : ctas_dim<256>(e4m3, rows);
     if (p.grid < p.row_tiles) p.grid = p.row_tiles;
     p.min_tiles = p.tc ? 1 : 2;
     return p;
 }
 
+template <int D, bool E4M3, int NT>
+cudaError_t launch_mma(const TreeArgs& a, cudaStream_t s) {
+    using C = Config<D, E4M3, NT>;
+    cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    tree_kernel<D, E4M3, NT><<<a.grid, kThreads, C::kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int D, bool E4M3>
 cudaError_t launch_config(const TreeArgs& a, bool tc, cudaStream_t s) {
-    using C = Config<D, E4M3>;
-    cudaError_t e;
     const int rows = a.max_nodes * (a.H / a.c.Hk);
     const dim3 join(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps);
-    if (tc) {
-        if ((e = launch_tree_tc(a, s)) != cudaSuccess) return e;
-        return launch_pdl(join_kernel<D, kTcRows, (D == 256 ? 64 : 128)>, join, dim3(kThreads), 0, s, a);
-    }
-    e = cudaFuncSetAttribute(tree_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = tc ? launch_tree_tc(a, s) : rows <= 8 ? launch_mma<D, E4M3, 1>(a, s) : launch_mma<D, E4M3, 2>(a, s);
     if (e != cudaSuccess) return e;
-    tree_kernel<D, E4M3><<<a.grid, kThreads, C::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (tc) return launch_pdl(join_kernel<D, kTcRows, (D == 256 ? 64 : 128)>, join, dim3(kThreads), 0, s, a);
     return launch_pdl(join_kernel<D, kRows, kTile>, join, dim3(kThreads), 0, s, a);
 }
 

@@ -21,6 +21,7 @@ constexpr int kTcRows = 128;    // query rows of a row tile (tcgen05 kernel)
 constexpr int kMaxRowTiles = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;  // growth of a row's largest weight (log2) that moves its reference
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
@@ -32,6 +33,35 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+
+// f16x2 of the two e4m3 codes in the low half of x (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// log2 of a value row's scale for the running reference: kept within +-100, so
+// that a weight without its scale stays in fp32's range.
+__device__ __forceinline__ float log2_scale(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return fminf(fmaxf(y, -100.f), 100.f);
+}
+
+// Zeroes the halves of a bf16 pair that are not finite; true if there was one.
+__device__ __forceinline__ bool zero_non_finite(uint32_t& x) {
+    const uint32_t y = x;
+    if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+    if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+    return x != y;
 }
 
 // bf16x2 of the two e4m3 codes in the high bytes of x's halves: sign to sign,

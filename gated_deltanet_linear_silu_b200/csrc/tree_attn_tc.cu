@@ -35,7 +35,6 @@ constexpr int kSoftWarps = 4, kMmaWarp = 4, kProdWarp0 = 5, kProdWarps = 8;
 constexpr int kTcThreads = 32 * (kProdWarp0 + kProdWarps);
 constexpr int kProdThreads = 32 * kProdWarps;
 constexpr int kScaleSlots = 4;
-constexpr float kLazy = 8.f;  // growth of a row's maximum (log2) that moves its reference
 constexpr uint64_t kDrainWaitNs = 1000000000ull;
 
 template <int D>
@@ -73,13 +72,13 @@ static_assert(sizeof(TcBars) <= 256, "barrier block");
 
 __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     if (limit == 0) return mbar_test_wait(bar, parity);
-    if (mbar_try_wait_sleep(bar, parity, 200000u)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 200000u)) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > limit) return false;
+    for (;;) {
+        for (int k = 0; k < 32; ++k)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag || globaltimer_ns() - t0 > limit) return false;
     }
-    return true;
 }
 
 // The same for a whole warp: one lane waits, all of them learn the outcome.
