@@ -1,25 +1,34 @@
 // Attention of a drafted tree over the paged cache, on the tensor cores' tcgen05
-// path (formula in tree_attn.cu).
+// path (formula in tree_attn.cu): more than 16 query rows of a key/value head.
 //
-// A unit is (sequence, key/value head, 128 query rows): rows are (node, query
-// head of the group) pairs, the M side of the products. One persistent CTA per
-// SM walks an equal share of the 128-token (D = 256: 64-token) tiles of its row
-// tile's line; 13 warps:
-//   warps 0-3   softmax, a row per thread: scores from tensor memory, running
-//               maximum and sum, probabilities back to tensor memory as bf16;
-//               the output at the end of a segment
-//   warp 4      issues the products: S = Q K^T of tile i + 1 goes out before
-//               O += P V of tile i, so that the next scores form meanwhile
-//   warps 5-12  producers: cache rows (page by page) into the shared-memory
-//               tiles the products read. bf16 rows by cp.async; e4m3 rows
-//               through registers (the loads of the next tile in flight while
-//               this one is converted), bf16 exactly
-// The output accumulates in tensor memory under a reference maximum that is
-// only moved (and the output rescaled) when a row's maximum outgrows it by 2^8,
-// which fp32 sums and bf16's exponent range absorb.
+// A unit is (sequence, key/value head, 128 query rows), rows the M side of the
+// products. One persistent CTA per SM walks an equal share of its row tile's
+// line in tiles of TN tokens; 14 warps:
+//   warps 0-7    softmax: two warps per 32 rows, half of the tile's tokens each,
+//                a row per thread; probabilities back to tensor memory; the
+//                output at the end of a segment
+//   warp 8       issues the products: S = Q K^T of tile i + 1 goes out before
+//                O += P V of tile i, so that the next scores form meanwhile
+//   warp 9       loader: the tile's pages, a lane per page. bf16 tiles go
+//                straight to their slots by TMA (128-byte swizzle); e4m3 pages
+//                by bulk copies into a raw ring
+//   warps 10-13  e4m3: raw tiles to f16 (exact) in the layout of the products;
+//                bf16: the tiles that hold drafted tokens or end the sequence,
+//                where rows past its end and drafted values that are not finite
+//                must be zero. Both: the queries
+// Tiles stand in one ring of slots in the order K0, V0, K1, V1, ..., so that the
+// keys of the next tiles do not wait for the values of this one.
+//
+// Scales, f16 and the reference R are those of tree_attn.cu. Two warps share a
+// row's reference: they vote at a named barrier on whether it has to move, and
+// only then exchange maxima and rescale the output in tensor memory.
 //
 // Every wait is bounded (gdn_set_wait_limit_ns).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cfloat>
+#include <mutex>
 
 #include "kv_page.cuh"
 #include "launch.h"
@@ -31,44 +40,51 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kProdWarp0 = 5, kProdWarps = 8;
-constexpr int kTcThreads = 32 * (kProdWarp0 + kProdWarps);
-constexpr int kProdThreads = 32 * kProdWarps;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kConvWarp0 = 10, kConvWarps = 4;
+constexpr int kTcThreads = 32 * (kConvWarp0 + kConvWarps), kConvThreads = 32 * kConvWarps;
 constexpr int kScaleSlots = 4;
 constexpr uint64_t kDrainWaitNs = 1000000000ull;
 
-template <int D>
+template <int D, bool E4M3>
 struct Tc {
     static constexpr int TN = D == 256 ? 64 : 128;  // tokens of a tile
-    static constexpr int kBlockQ = kTcRows * 128;   // 64 elements of every row
+    static constexpr int kBlockQ = kTcRows * 128;   // 64 elements of every row, 128-byte swizzled
     static constexpr int kBlock = TN * 128;
     static constexpr int kBlocks = D / 64;
-    static constexpr int kQ = kBlockQ * kBlocks, kTileBytes = kBlock * kBlocks;
-    static constexpr int kOffK = kQ, kOffV = kOffK + 2 * kTileBytes, kOffScale = kOffV + 2 * kTileBytes;
-    static constexpr int kOffBars = kOffScale + kScaleSlots * 2 * TN * 4;
-    static constexpr int kUsed = kOffBars + 256 + 1024;  // 1024: alignment
+    static constexpr int kQ = kBlockQ * kBlocks, kSlot = kBlock * kBlocks;
+    static constexpr int kSlots = E4M3 ? (D == 256 ? 3 : 4) : (D == 256 ? 5 : 6);
+    // raw e4m3 tiles: TN rows of D bytes, then TN scales
+    static constexpr int kRaw = TN * D + TN * 4, kRawSlots = 3;
+    static constexpr int kOffSlots = kQ, kOffRaw = kOffSlots + kSlots * kSlot;
+    static constexpr int kOffScale = kOffRaw + (E4M3 ? kRawSlots * kRaw : 0);  // [slot][k, v, log2 v][TN]
+    static constexpr int kScaleBytes = E4M3 ? kScaleSlots * 3 * TN * 4 : 0;
+    static constexpr int kOffRows = kOffScale + kScaleBytes;      // maxima [2][128], row factors [2][128] (e4m3)
+    static constexpr int kOffBars = kOffRows + (E4M3 ? 4 : 2) * 128 * 4;
+    static constexpr int kUsed = kOffBars + 352 + 1024;           // 1024: alignment
     // above half of the SM's shared memory, so that a CTA has its tensor memory to itself
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
     static constexpr int kColS = D == 256 ? 256 : 128;  // S buffers behind O
-    static constexpr uint32_t kIdescS = idesc_bf16(128, TN, 0, 0);
-    static constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1);
+    static constexpr uint32_t kFormat = E4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16 operands: format bits 0
+    static constexpr uint32_t kIdescS = idesc_bf16(128, TN, 0, 0) & kFormat;
+    static constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1) & kFormat;
 };
 
 struct TcBars {
-    uint64_t kfull[2], kempty[2];  // producers (8 warps) / commit
-    uint64_t vfull[2], vempty[2];
-    uint64_t sfull[2];             // scores of a tile (commit)
-    uint64_t pfull[2];             // its probabilities (4 warps)
-    uint64_t odone;                // output product of a tile done (commit)
-    uint64_t ofree;                // a segment's output read (4 warps)
-    uint64_t qfull, qempty;        // a segment's queries (8 warps / commit)
-    uint64_t cfull[kScaleSlots];   // a tile's scales (8 warps)
+    uint64_t full[6], empty[6];      // slots of the products (4 converter warps, bf16: and the loader / commit)
+    uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / 4 warps)
+    uint64_t hand[6];                // bf16: slot left to the converters (loader)
+    uint64_t sfull[2], pfull[2];     // scores (commit), probabilities (8 warps)
+    uint64_t odone, ofree;           // output product (commit), output read (8 warps)
+    uint64_t qfull, qempty;          // queries (4 warps / commit)
+    uint64_t cfull[kScaleSlots];     // a tile's scales (4 warps)
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
-    int odd;                       // some drafted value was not finite
+    int odd;                         // some drafted value was not finite
+    int gave_up[kSoftWarps];         // a softmax warp whose wait ran out, for its partner
 };
-static_assert(sizeof(TcBars) <= 256, "barrier block");
+static_assert(sizeof(TcBars) <= 352, "barrier block");
 
 __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     if (limit == 0) return mbar_test_wait(bar, parity);
@@ -80,13 +96,40 @@ __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile in
         if (*abort_flag || globaltimer_ns() - t0 > limit) return false;
     }
 }
-
 // The same for a whole warp: one lane waits, all of them learn the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     const bool ok = (threadIdx.x & 31) != 0 || tc_wait(bar, parity, abort_flag, limit);
     return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// The 64 softmax threads of two warps with the same rows, at their named barrier.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(y)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return y != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&y);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&y);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -101,56 +144,61 @@ __device__ __forceinline__ uint32_t sees32(uint64_t sees, int off) {
     return (uint32_t)(sees << -off) | ((1u << -off) - 1u);
 }
 
-// 16 e4m3 codes as 16 bf16, each four in the order 0, 2, 1, 3.
-__device__ __forceinline__ void convert16(const uint4& u, uint4 (&out)[2]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = e4m3_hi_to_bf16x2(w[i] << 8);
-        y[2 * i + 1] = e4m3_hi_to_bf16x2(w[i]);
-    }
-    out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
-    using C = Tc<D>;
+__global__ void __launch_bounds__(kTcThreads, 1)
+tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v) {
+    using C = Tc<D, E4M3>;
     constexpr int TN = C::TN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     TcBars& B = *reinterpret_cast<TcBars*>(sm + C::kOffBars);
     volatile int* abort_flag = &B.abort_flag;
-    float* scales = reinterpret_cast<float*>(sm + C::kOffScale);  // [slot][k then v][TN]
+    float* scales = reinterpret_cast<float*>(sm + C::kOffScale);
+    float* row_top = reinterpret_cast<float*>(sm + C::kOffRows);  // [half][row]
+    float* row_mul = row_top + 256;                               // [segment parity][row] (e4m3)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.H / a.c.Hk;
     const uint64_t wlim = a.wait_ns;
     pdl_launch_dependents();
 
     if (tid == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&B.full[i], E4M3 ? kConvWarps : kConvWarps + 1);
+            mbar_init(&B.empty[i], 1);
+            mbar_init(&B.hand[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&B.rfull[i], 1);
+            mbar_init(&B.rempty[i], kConvWarps);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&B.kfull[i], kProdWarps);
-            mbar_init(&B.kempty[i], 1);
-            mbar_init(&B.vfull[i], kProdWarps);
-            mbar_init(&B.vempty[i], 1);
             mbar_init(&B.sfull[i], 1);
             mbar_init(&B.pfull[i], kSoftWarps);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], kProdWarps);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], kConvWarps);
         mbar_init(&B.odone, 1);
         mbar_init(&B.ofree, kSoftWarps);
-        mbar_init(&B.qfull, kProdWarps);
+        mbar_init(&B.qfull, kConvWarps);
         mbar_init(&B.qempty, 1);
         mbar_init(&B.drain, 1);
         fence_mbar_init();
         B.abort_flag = 0;
         B.odd = 0;
+        for (int i = 0; i < kSoftWarps; ++i) B.gave_up[i] = 0;
     }
     if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
     tc_fence_before();
-    const Share share = find_share<kTcRows, TN, kTcThreads>(a);
-    tc_fence_after();  // (find_share synchronises the CTA)
+    const Share share = find_share<kTcRows, TN, kTcThreads>(a);  // (synchronises the CTA)
+    tc_fence_after();
     const uint32_t tmem = B.tmem;
     auto fail = [&]() {
         if (!*abort_flag) {
@@ -158,244 +206,228 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
             set_status(a.status, kStatusTimeout);
         }
     };
+    const int page = 1 << a.c.page_shift;
+    const int run = page < TN ? page : TN;  // tokens of one page in a tile
+    // bf16 tiles that the converters fill: with drafted tokens, or past the sequence's end
+    auto by_hand = [&](const Segment& g, int tile) {
+        return !E4M3 && (tile + 1) * TN > g.seq.len - g.seq.nodes;
+    };
+    Segment seg;
+    bool have = first_segment<kTcRows, TN>(a, share, seg);
+    bool ok = true;
 
-    if (warp >= kProdWarp0) {
-        // ============================================================ producers
-        const int pt = tid - 32 * kProdWarp0;
-        constexpr int kElem = E4M3 ? 1 : 2;
-        constexpr int kPer = D * kElem / 16;                     // 16-byte pieces of a row
-        constexpr int kPieces = TN * kPer / kProdThreads;        // of a thread, per tile
-        constexpr int kTokStep = kProdThreads / kPer;            // tokens between its pieces
-        const int tok0 = pt / kPer, col = pt % kPer;
-        bool ok = true;
-        int64_t i = 0;  // tile number in this CTA
-        int seg_no = 0;
-        Segment seg;
-        bool have = first_segment<kTcRows, TN>(a, share, seg);
-        // Cache row of each of this thread's tokens of the tile at pos, -1: zeros.
-        // (The C ABI keeps a cache's rows below 2^31.)
-        auto rows_of = [&](const Segment& g, int pos, int (&row)[kPieces]) {
+    if (warp == kLoadWarp) {
+        // ================================================================ loader
+        if (!E4M3 && lane == 0) {
+            prefetch_tmap(&map_k);
+            prefetch_tmap(&map_v);
+        }
+        int x = 0;                               // group: tile x / 2's keys (even) or values
+        uint32_t last_full = 0, last_par = 0;    // copies in flight, for the end
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
+            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
+                // this lane's page of the tile
+                const int pos = tile * TN + lane * run;
+                const int n_runs = min(TN / run, (min(TN, seg.seq.len - tile * TN) + run - 1) / run);
+                int row = 0;
+                if (lane < n_runs) {
+                    row = (int)page_row(a.p, a.c, seg.n, pos);
+                    if (row < 0) {
+                        set_status(a.status, kStatusBadSeqlens);
+                        row = 0;  // some rows of the pool: the sequence's output means nothing
+                    } else {
+                        row += seg.hk << a.c.page_shift;
+                    }
+                }
 #pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                const int p = pos + tok0 + j * kTokStep;
-                row[j] = -1;
-                if (p < g.seq.len) {
-                    row[j] = (int)page_row(a.p, a.c, g.n, p);
-                    if (row[j] < 0) set_status(a.status, kStatusBadSeqlens);
-                    else row[j] += g.hk << a.c.page_shift;
+                for (int kv = 0; kv < 2; ++kv, ++x) {
+                    if (E4M3) {
+                        const int st = x % C::kRawSlots, use = x / C::kRawSlots;
+                        if (!warp_wait(&B.rempty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        uint8_t* dst = sm + C::kOffRaw + st * C::kRaw;
+                        if (lane == 0) mbar_arrive_expect_tx(&B.rfull[st], (uint32_t)(n_runs * run * (D + 4)));
+                        last_full |= 1u << st;
+                        last_par = (last_par & ~(1u << st)) | (uint32_t)(use & 1) << st;
+                        __syncwarp();
+                        if (lane < n_runs) {
+                            bulk_load(dst + lane * run * D, static_cast<const uint8_t*>(kv ? a.c.v : a.c.k) + (int64_t)row * D,
+                                      run * D, &B.rfull[st]);
+                            bulk_load(dst + TN * D + lane * run * 4, (kv ? a.c.v_scale : a.c.k_scale) + row, run * 4,
+                                      &B.rfull[st]);
+                        }
+                    } else {
+                        const int st = x % C::kSlots, use = x / C::kSlots;
+                        if (!warp_wait(&B.empty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        if (by_hand(seg, tile)) {  // (the converters walk only these: a slot's phases are followed here)
+                            if (lane == 0) {
+                                mbar_arrive(&B.full[st]);
+                                mbar_arrive(&B.hand[st]);
+                            }
+                            continue;
+                        }
+                        uint8_t* dst = sm + C::kOffSlots + st * C::kSlot + lane * run * 128;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&B.full[st], C::kSlot);
+                            mbar_arrive_n(&B.full[st], kConvWarps);
+                        }
+                        last_full |= 1u << st;
+                        last_par = (last_par & ~(1u << st)) | (uint32_t)(use & 1) << st;
+                        __syncwarp();
+                        if (lane < n_runs) {
+#pragma unroll
+                            for (int b = 0; b < C::kBlocks; ++b)
+                                tma_load_2d(dst + b * C::kBlock, kv ? &map_v : &map_k, &B.full[st], 64 * b, row);
+                        }
+                    }
                 }
             }
-        };
-        auto load_queries = [&](const Segment& g) -> bool {
-            if (seg_no > 0 && !warp_wait(&B.qempty, (seg_no - 1) & 1, abort_flag, wlim)) return false;
-            for (int x = pt; x < kTcRows * (D / 8); x += kProdThreads) {
-                const int m = x / (D / 8), c8 = x % (D / 8);
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (m < g.rows) {
-                    const int r = g.rt * kTcRows + m;
-                    const int64_t t = g.seq.first + r / G;
-                    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
-                                                       (int64_t)(g.hk * G + r % G) * D + 8 * c8);
-                    if (E4M3)
-                        u = make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632),
-                                       __byte_perm(u.z, u.w, 0x5410), __byte_perm(u.z, u.w, 0x7632));
-                }
-                *reinterpret_cast<uint4*>(sm + (c8 >> 3) * C::kBlockQ + sw128_off(m, c8 & 7)) = u;
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.qfull);
-            return true;
-        };
+        }
+        if (!ok) fail();
+        // no copy may land after the CTA is gone
+        if (lane == 0)
+            for (int st = 0; st < 6; ++st)
+                if ((last_full >> st) & 1)
+                    mbar_wait(E4M3 ? &B.rfull[st < 3 ? st : 0] : &B.full[st], (last_par >> st) & 1, kDrainWaitNs);
+        __syncwarp();
+    } else if (warp >= kConvWarp0) {
+        // ========================================== queries, conversion, last tiles
+        const int pt = tid - 32 * kConvWarp0;
+        int x = 0, seg_no = 0;
+        uint32_t hand_par = 0;  // per slot: phase of its next hand-over
         auto publish = [&](uint64_t* bar) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        if (E4M3) {
-            uint4 kr[kPieces], vr[kPieces];
-            float ks = 0.f, vs = 0.f;
-            int row[kPieces];
-            const float scale2 = a.scale * kLog2e;
-            auto load_k = [&]() {
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg), ++seg_no) {
+            if (seg_no > 0 && !warp_wait(&B.qempty, (seg_no - 1) & 1, abort_flag, wlim)) { ok = false; break; }
+            constexpr int kQPer = D / 8;  // 16-byte pieces of a query row: as many lanes
+#pragma unroll 2
+            for (int y = pt; y < kTcRows * kQPer; y += kConvThreads) {
+                const int m = y / kQPer, c8 = y % kQPer;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (m < seg.rows) {
+                    const int r = seg.rt * kTcRows + m;
+                    const int64_t t = seg.seq.first + r / G;
+                    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
+                                                       (int64_t)(seg.hk * G + r % G) * D + 8 * c8);
+                }
+                if (E4M3) {
+                    // to f16, the row scaled by a power of two that puts its largest element in [1, 2)
+                    uint32_t w[4] = {u.x, u.y, u.z, u.w}, top = 0;
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j)
-                    kr[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0)
-                                       : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.k) + (int64_t)row[j] * D) + col);
-            };
-            auto load_v = [&]() {
+                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j)
-                    vr[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0)
-                                       : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c.v) + (int64_t)row[j] * D) + col);
-            };
-            auto load_scales = [&](const Segment& g, int pos) {
-                if (pt < TN) {
-                    ks = vs = 0.f;
-                    if (pos + pt < g.seq.len) {
-                        int64_t r = page_row(a.p, a.c, g.n, pos + pt);
-                        if (r >= 0) {
-                            r += (int64_t)g.hk << a.c.page_shift;
-                            ks = __ldg(a.c.k_scale + r) * scale2;
-                            vs = __ldg(a.c.v_scale + r);
+                    for (int o = kQPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    uint32_t ex = top >> 7;  // a row that is not finite stays as it is
+                    ex = ex == 255u || top == 0u ? 127u : ex < 1u ? 1u : ex > 253u ? 253u : ex;
+                    const float down = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack_f16(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xFFFF0000u) * down);
+                    u = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (c8 == 0) row_mul[(seg_no & 1) * 128 + m] = __uint_as_float(ex << 23) * a.scale * kLog2e;
+                }
+                *reinterpret_cast<uint4*>(sm + (c8 >> 3) * C::kBlockQ + sw128_off(m, c8 & 7)) = u;
+            }
+            publish(&B.qfull);
+            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
+                const int left = seg.seq.len - tile * TN;  // tokens that exist, from the tile's first
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++x) {
+                    const int st = x % C::kSlots;
+                    uint8_t* slot = sm + C::kOffSlots + st * C::kSlot;
+                    if (E4M3) {
+                        const int rs = x % C::kRawSlots;
+                        if (!warp_wait(&B.rfull[rs], (x / C::kRawSlots) & 1, abort_flag, wlim)) { ok = false; break; }
+                        const uint8_t* raw = sm + C::kOffRaw + rs * C::kRaw;
+                        if (pt < TN) {
+                            const float s = reinterpret_cast<const float*>(raw + TN * D)[pt];
+                            float* out = scales + ((x >> 1) % kScaleSlots) * 3 * TN;
+                            out[kv * TN + pt] = pt < left ? s : 0.f;
+                            if (kv) out[2 * TN + pt] = log2_scale(pt < left ? s : 0.f);
                         }
-                    }
-                }
-            };
-            auto store = [&](uint8_t* tile, const uint4 (&x)[kPieces]) {
+                        if (kv) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&B.cfull[(x >> 1) % kScaleSlots]);
+                        }
+                        if (!warp_wait(&B.empty[st], ((x / C::kSlots) & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        constexpr int kPer = D / 16, kPieces = TN * kPer / kConvThreads, kAhead = 4;
+                        const int col = pt % kPer, tok0 = pt / kPer;
+                        // neighbouring blocks start with the other half: eight lanes, eight bank groups
+                        const int f = (col >> 2) & 1, c16 = 2 * (col & 3);
+#pragma unroll 1
+                        for (int j0 = 0; j0 < kPieces; j0 += kAhead) {
+                            uint4 u[kAhead];
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    uint4 y[2];
-                    convert16(x[j], y);
-                    const int tok = tok0 + j * kTokStep;
-                    uint8_t* p = tile + (col >> 2) * C::kBlock;
-                    // neighbouring blocks start with the other half: eight lanes, eight banks groups
-                    const int f = (col >> 2) & 1, c16 = 2 * (col & 3);
-                    *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + f)) = f ? y[1] : y[0];
-                    *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + 1 - f)) = f ? y[0] : y[1];
-                }
-            };
-            int tile = 0;
-            if (have) {
-                tile = seg.tile0;
-                rows_of(seg, tile * TN, row);
-                load_scales(seg, tile * TN);
-                load_k();
-                load_v();
-            }
-            while (ok && have) {
-                if (tile == seg.tile0 && !load_queries(seg)) { ok = false; break; }
-                const int st = (int)(i & 1), par = (int)((i >> 1) & 1);
-                // the tile after this one
-                Segment next = seg;
-                int next_tile = tile + 1;
-                bool more = true;
-                if (next_tile == seg.tile1) {
-                    more = next_segment<kTcRows, TN>(a, share, next);
-                    next_tile = next.tile0;
-                }
-                if (!warp_wait(&B.kempty[st], par ^ 1, abort_flag, wlim)) { ok = false; break; }
-                store(sm + C::kOffK + st * C::kTileBytes, kr);
-                if (pt < TN) {
-                    float* s = scales + (i % kScaleSlots) * 2 * TN;
-                    s[pt] = ks;
-                    s[TN + pt] = vs;
-                }
-                publish(&B.kfull[st]);
-                if (lane == 0) mbar_arrive(&B.cfull[i % kScaleSlots]);
-                if (more) {
-                    rows_of(next, next_tile * TN, row);
-                    load_scales(next, next_tile * TN);
-                    load_k();
-                }
-                if (!warp_wait(&B.vempty[st], par ^ 1, abort_flag, wlim)) { ok = false; break; }
-                store(sm + C::kOffV + st * C::kTileBytes, vr);
-                publish(&B.vfull[st]);
-                if (more) load_v();
-                ++i;
-                if (next_tile == next.tile0 && more) ++seg_no;
-                seg = next;
-                tile = next_tile;
-                have = more;
-            }
-        } else {
-            // groups of copies in order K0, V0, K1, V1, ...: a group is published once the two
-            // issued after it are under way
-            int64_t issued = 0, done = 0;  // groups; K and V of the CTA's tile x are 2 x and 2 x + 1
-            int drafts[2] = {0, 0};        // of a V stage: 0, or its first drafted token's place + 1
-            auto copy = [&](uint8_t* tile, const void* src, const int (&row)[kPieces]) {
+                            for (int j = 0; j < kAhead; ++j) {
+                                const int tok = tok0 + (j0 + j) * (kConvThreads / kPer);
+                                u[j] = *reinterpret_cast<const uint4*>(raw + tok * D + 16 * col);
+                                if (tok >= left) u[j] = make_uint4(0, 0, 0, 0);
+                            }
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    const uint8_t* s = static_cast<const uint8_t*>(src) + (int64_t)(row[j] < 0 ? 0 : row[j]) * (2 * D) + 16 * col;
-                    cp_async_zfill16(tile + (col >> 3) * C::kBlock + sw128_off(tok0 + j * kTokStep, col & 7), s,
-                                     row[j] >= 0);
-                }
-                cp_async_commit_group();
-            };
-            // Publishes group g; drafted values that are not finite become zero first (the rows that
-            // see them get them at the end of the segment).
-            auto finish = [&](int64_t g) {
-                const int st = (int)((g >> 1) & 1);
-                if (g & 1) {
-                    const int draft_pos = drafts[st];
-                    if (draft_pos) {
-                        uint8_t* tile = sm + C::kOffV + st * C::kTileBytes;
-                        bool odd = false;
-#pragma unroll
-                        for (int j = 0; j < kPieces; ++j) {
-                            const int tok = tok0 + j * kTokStep;
-                            if (tok < draft_pos - 1) continue;
-                            uint32_t* w = reinterpret_cast<uint32_t*>(tile + (col >> 3) * C::kBlock + sw128_off(tok, col & 7));
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t x = w[e];
-                                const uint32_t y = x;
-                                if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-                                if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-                                if (x != y) {
-                                    w[e] = x;
-                                    odd = true;
-                                }
+                            for (int j = 0; j < kAhead; ++j) {
+                                const int tok = tok0 + (j0 + j) * (kConvThreads / kPer);
+                                const uint4 lo = make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
+                                                            e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
+                                const uint4 hi = make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
+                                                            e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
+                                uint8_t* p = slot + (col >> 2) * C::kBlock;
+                                *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + f)) = f ? hi : lo;
+                                *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + 1 - f)) = f ? lo : hi;
                             }
                         }
+                        publish(&B.full[st]);
+                        if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
+                    } else {
+                        if (!by_hand(seg, tile)) continue;
+                        if (!warp_wait(&B.hand[st], (hand_par >> st) & 1, abort_flag, wlim)) { ok = false; break; }
+                        hand_par ^= 1u << st;
+                        constexpr int kPer = D / 8;
+                        const int draft = seg.seq.len - seg.seq.nodes - tile * TN;  // the draft's first token here
+                        bool odd = false;
+#pragma unroll 2
+                        for (int y = pt; y < TN * kPer; y += kConvThreads) {
+                            const int tok = y / kPer, col = y % kPer;
+                            uint4 u = make_uint4(0, 0, 0, 0);
+                            if (tok < left) {
+                                const int64_t row = page_row(a.p, a.c, seg.n, tile * TN + tok);
+                                if (row < 0) set_status(a.status, kStatusBadSeqlens);
+                                else
+                                    u = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(kv ? a.c.v : a.c.k) +
+                                                                         (row + ((int64_t)seg.hk << a.c.page_shift)) * D) + col);
+                            }
+                            if (kv && tok >= draft) {
+                                odd |= zero_non_finite(u.x);
+                                odd |= zero_non_finite(u.y);
+                                odd |= zero_non_finite(u.z);
+                                odd |= zero_non_finite(u.w);
+                            }
+                            *reinterpret_cast<uint4*>(slot + (col >> 3) * C::kBlock + sw128_off(tok, col & 7)) = u;
+                        }
                         if (odd) *reinterpret_cast<volatile int*>(&B.odd) = 1;
-                    }
-                    publish(&B.vfull[st]);
-                } else {
-                    publish(&B.kfull[st]);
-                }
-            };
-            while (ok && have) {
-                if (!load_queries(seg)) { ok = false; break; }
-                const int base = seg.seq.len - seg.seq.nodes;
-                for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++i) {
-                    const int st = (int)(i & 1), par = (int)((i >> 1) & 1);
-                    int row[kPieces];
-                    rows_of(seg, tile * TN, row);
-                    if (!warp_wait(&B.kempty[st], par ^ 1, abort_flag, wlim)) { ok = false; break; }
-                    copy(sm + C::kOffK + st * C::kTileBytes, a.c.k, row);
-                    if (++issued - done > 2) {
-                        cp_async_wait_group<2>();
-                        finish(done++);
-                    }
-                    if (!warp_wait(&B.vempty[st], par ^ 1, abort_flag, wlim)) { ok = false; break; }
-                    const int from = base - tile * TN;  // the draft's first token in this tile
-                    drafts[st] = from < TN ? (from > 0 ? from : 0) + 1 : 0;
-                    copy(sm + C::kOffV + st * C::kTileBytes, a.c.v, row);
-                    if (++issued - done > 2) {
-                        cp_async_wait_group<2>();
-                        finish(done++);
+                        publish(&B.full[st]);
                     }
                 }
-                if (!ok) break;
-                // nothing may hold back the segment's last groups: the next one's queries wait for them
-                cp_async_wait_group<0>();
-                while (done < issued) finish(done++);
-                ++seg_no;
-                have = next_segment<kTcRows, TN>(a, share, seg);
             }
         }
         if (!ok) fail();
-        cp_async_wait_group<0>();
     } else if (warp == kMmaWarp) {
         // ================================================================ products
         if (lane == 0) {
-            bool ok = true;
-            Segment seg;
-            bool have = first_segment<kTcRows, TN>(a, share, seg);
-            int64_t i = 0;
-            int seg_no = 0;
-            auto scores = [&](int64_t x, bool first, bool last, int sn) -> bool {  // S of tile x
-                const int st = (int)(x & 1);
+            int i = 0, seg_no = 0;
+            auto scores = [&](int x, bool first, bool last, int sn) -> bool {  // S of tile x
+                const int g = 2 * x, st = g % C::kSlots, b = x & 1;
                 if (first && !tc_wait(&B.qfull, sn & 1, abort_flag, wlim)) return false;
-                if (!tc_wait(&B.kfull[st], (x >> 1) & 1, abort_flag, wlim)) return false;
+                if (!tc_wait(&B.full[st], (g / C::kSlots) & 1, abort_flag, wlim)) return false;
                 tc_fence_after();
-                const uint32_t k0 = smem_u32(sm + C::kOffK + st * C::kTileBytes), q0 = smem_u32(sm);
+                const uint32_t k0 = smem_u32(sm + C::kOffSlots + st * C::kSlot), q0 = smem_u32(sm);
 #pragma unroll 4
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tmem + C::kColS + st * TN, sw128_desc(q0 + (kk >> 2) * C::kBlockQ + 32 * (kk & 3), 16, 1024),
+                    mma_bf16(tmem + C::kColS + b * TN, sw128_desc(q0 + (kk >> 2) * C::kBlockQ + 32 * (kk & 3), 16, 1024),
                              sw128_desc(k0 + (kk >> 2) * C::kBlock + 32 * (kk & 3), 16, 1024), C::kIdescS, kk > 0);
-                mma_commit(&B.sfull[st]);
-                mma_commit(&B.kempty[st]);
+                mma_commit(&B.sfull[b]);
+                mma_commit(&B.empty[st]);
                 if (last) mma_commit(&B.qempty);
                 return true;
             };
@@ -411,24 +443,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
                     next_tile = next.tile0;
                 }
                 if (!crosses && !scores(i + 1, false, next_tile + 1 == seg.tile1, seg_no)) { ok = false; break; }
-                const int st = (int)(i & 1);
-                if (tile == seg.tile0 && seg_no > 0 && !tc_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim)) {
-                    ok = false;
-                    break;
-                }
-                if (!tc_wait(&B.pfull[st], (i >> 1) & 1, abort_flag, wlim) ||
-                    !tc_wait(&B.vfull[st], (i >> 1) & 1, abort_flag, wlim)) {
+                const int g = 2 * i + 1, st = g % C::kSlots, b = i & 1;
+                if ((tile == seg.tile0 && seg_no > 0 && !tc_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim)) ||
+                    !tc_wait(&B.pfull[b], (i >> 1) & 1, abort_flag, wlim) ||
+                    !tc_wait(&B.full[st], (g / C::kSlots) & 1, abort_flag, wlim)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t v0 = smem_u32(sm + C::kOffV + st * C::kTileBytes);
+                const uint32_t v0 = smem_u32(sm + C::kOffSlots + st * C::kSlot);
 #pragma unroll 4
                 for (int kk = 0; kk < TN / 16; ++kk)
-                    mma_bf16_ta(tmem, tmem + C::kColS + st * TN + 8 * kk, sw128_desc(v0 + 2048 * kk, C::kBlock, 1024),
+                    mma_bf16_ta(tmem, tmem + C::kColS + b * TN + 8 * kk, sw128_desc(v0 + 2048 * kk, C::kBlock, 1024),
                                 C::kIdescO, tile != seg.tile0 || kk > 0);
                 mma_commit(&B.odone);
-                mma_commit(&B.vempty[st]);
+                mma_commit(&B.empty[st]);
                 if (crosses && more) {
                     ++seg_no;
                     if (!scores(i + 1, true, next.tile1 - next.tile0 == 1, seg_no)) { ok = false; break; }
@@ -445,13 +474,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
         __syncwarp();
     } else {
         // ================================================================= softmax
-        const int m = tid;  // row of the tile, lane of tensor memory
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-        bool ok = true;
-        int64_t i = 0;
-        Segment seg;
-        for (bool have = first_segment<kTcRows, TN>(a, share, seg); ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
-            const bool busy = 32 * warp < seg.rows, live = m < seg.rows;
+        constexpr int HC = TN / 2;  // tokens of this warp's half
+        const int quarter = warp & 3, half = warp >> 2;
+        const int m = 32 * quarter + lane;  // row of the tile, lane of tensor memory
+        const int pair = 1 + quarter;       // named barrier of the two warps
+        const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+        int i = 0, seg_no = 0;
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg), ++seg_no) {
+            const bool busy = 32 * quarter < seg.rows, live = m < seg.rows;
             const int r = seg.rt * kTcRows + (live ? m : 0);
             const int node = r / G, head = seg.hk * G + r % G;
             const int64_t t = seg.seq.first + node;
@@ -461,54 +491,80 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
                 sees = a.mask ? (uint64_t)a.mask[t] : (2ull << node) - 1;
                 if (seg.seq.nodes < 64) sees &= (1ull << seg.seq.nodes) - 1;
             }
-            float ref = kNegInf, l = 0.f;  // reference maximum (log2 units), sum
-            const float scale2 = a.scale * kLog2e;
+            float ref = kNegInf, mul = a.scale * kLog2e;
+            float2 l2 = make_float2(0.f, 0.f);
             for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++i) {
-                const int st = (int)(i & 1);
-                if (!warp_wait(&B.sfull[st], (i >> 1) & 1, abort_flag, wlim) ||
-                    (E4M3 && !warp_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim))) {
-                    ok = false;
-                    break;
-                }
+                const int b = i & 1;
+                // A warp whose wait runs out goes on to the vote below, where its partner
+                // learns of it: neither may stay alone at their barrier.
+                ok = warp_wait(&B.sfull[b], (i >> 1) & 1, abort_flag, wlim) &&
+                     (!E4M3 || warp_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim)) && ok;
                 tc_fence_after();
                 if (busy) {
-                    const uint32_t s0 = tmem + lane_off + C::kColS + st * TN;
-                    const float* sc = scales + (i % kScaleSlots) * 2 * TN;
-                    const int off = tile * TN - base;  // the tile's start past the context
-                    const bool masked = off + TN > 0;
-                    float top = kNegInf;
+                    if (E4M3 && tile == seg.tile0) mul = live ? row_mul[(seg_no & 1) * 128 + m] : 0.f;
+                    const uint32_t s0 = tmem + lane_off + C::kColS + b * TN;
+                    const float* sc = scales + (i % kScaleSlots) * 3 * TN + half * HC;
+                    const int off = tile * TN + half * HC - base;  // this half's start past the context
+                    const bool masked = off + HC > 0;
+                    float2 s[HC / 2];
 #pragma unroll
-                    for (int c0 = 0; c0 < TN; c0 += 32) {
-                        float s[32];
-                        tmem_ld32(s0 + c0, s);
-                        tmem_wait_ld();
-                        if (E4M3) {
+                    for (int c0 = 0; c0 < HC; c0 += 32)
+                        tmem_ld32(s0 + half * HC + c0, *reinterpret_cast<float(*)[32]>(&s[c0 / 2]));
+                    tmem_wait_ld();
+                    const float2 mul_2 = make_float2(mul, mul);
+                    if (E4M3) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4*>(sc + c0 + e);
-                                s[e] *= k4.x; s[e + 1] *= k4.y; s[e + 2] *= k4.z; s[e + 3] *= k4.w;
-                            }
+                        for (int e = 0; e < HC / 2; e += 2) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * e);
+                            s[e] = mul2(s[e], mul2(mul_2, make_float2(k4.x, k4.y)));
+                            s[e + 1] = mul2(s[e + 1], mul2(mul_2, make_float2(k4.z, k4.w)));
                         }
-                        if (masked) {
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < HC / 2; ++e) s[e] = mul2(s[e], mul_2);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c0 = 0; c0 < HC; c0 += 32) {
                             const uint32_t bits = sees32(sees, off + c0);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1 ? s[e] : kNegInf;
+                            for (int e = 0; e < 16; ++e) {
+                                if (!((bits >> (2 * e)) & 1)) s[c0 / 2 + e].x = kNegInf;
+                                if (!((bits >> (2 * e + 1)) & 1)) s[c0 / 2 + e].y = kNegInf;
+                            }
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) top = max3(top, s[e], s[e + 1]);
                     }
-                    if (!E4M3) top *= scale2;
-                    // ---- the reference: moved when outgrown
-                    const bool move = ref == kNegInf ? top > kNegInf : top > ref + kLazy;
-                    if (__any_sync(0xffffffffu, move)) {
+                    float top = kNegInf, top_b = kNegInf;
+#pragma unroll
+                    for (int e = 0; e < HC / 2; e += 2) {
+                        float2 y = s[e], z = s[e + 1];
+                        if (E4M3) {
+                            const float4 v4 = *reinterpret_cast<const float4*>(sc + 2 * TN + 2 * e);
+                            y = add2(y, make_float2(v4.x, v4.y));
+                            z = add2(z, make_float2(v4.z, v4.w));
+                        }
+                        top = max3(top, y.x, y.y);
+                        top_b = max3(top_b, z.x, z.y);
+                    }
+                    top = fmaxf(top, top_b);
+                    // ---- the reference: moved when either half outgrows it (both warps have
+                    // read their scores when the vote is out: probabilities may overwrite them)
+                    if (pair_any(pair, !ok || (live && top > ref + kLazy))) {
+                        row_top[half * 128 + m] = top;
+                        if (!ok) B.gave_up[warp] = 1;
+                        pair_sync(pair);
+                        ok = ok && !B.gave_up[warp ^ 4];
+                        if (!ok) break;
+                        top = fmaxf(top, row_top[(half ^ 1) * 128 + m]);
+                        const bool move = top > ref;
                         const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
                         if (move) ref = top;
-                        l *= f;
-                        if (tile != seg.tile0 && __any_sync(0xffffffffu, f != 1.f)) {
-                            if (!warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) { ok = false; break; }
+                        l2 = mul2(l2, make_float2(f, f));
+                        if (tile != seg.tile0) {
+                            if (!warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) ok = false;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
+                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                                 float o[32];
                                 tmem_ld32(tmem + lane_off + c0, o);
                                 tmem_wait_ld();
@@ -518,74 +574,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
                             }
                             tmem_wait_st();
                         }
+                        pair_sync(pair);  // the maxima are read
                     }
                     const float minus = ref == kNegInf ? 0.f : -ref;
+                    const float2 minus_2 = make_float2(minus, minus);
 #pragma unroll
-                    for (int c0 = 0; c0 < TN; c0 += 32) {
-                        float s[32];
-                        tmem_ld32(s0 + c0, s);
-                        tmem_wait_ld();
-                        const uint32_t bits = masked ? sees32(sees, off + c0) : 0xFFFFFFFFu;
+                    for (int c0 = 0; c0 < HC; c0 += 32) {
+                        const uint32_t bits = E4M3 && masked ? sees32(sees, off + c0) : 0xFFFFFFFFu;
                         uint32_t p[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 k4 = make_float4(scale2, scale2, scale2, scale2), v4 = make_float4(1.f, 1.f, 1.f, 1.f);
+                        for (int e = 0; e < 16; e += 2) {
+                            float2 y = add2(s[c0 / 2 + e], minus_2), z = add2(s[c0 / 2 + e + 1], minus_2);
+                            y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                            l2 = add2(l2, add2(y, z));
                             if (E4M3) {
-                                k4 = *reinterpret_cast<const float4*>(sc + c0 + e);
-                                v4 = *reinterpret_cast<const float4*>(sc + TN + c0 + e);
+                                const float4 v4 = *reinterpret_cast<const float4*>(sc + TN + c0 + 2 * e);
+                                y = mul2(y, make_float2(v4.x, v4.y));
+                                z = mul2(z, make_float2(v4.z, v4.w));
+                                if (masked) {  // nothing from a token that the row does not see, whatever its scale
+                                    if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
+                                    if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
+                                    if (!((bits >> (2 * e + 2)) & 1)) z.x = 0.f;
+                                    if (!((bits >> (2 * e + 3)) & 1)) z.y = 0.f;
+                                }
                             }
-                            const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
-                            float w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                float q = exp2_approx(fmaf(s[e + x], kk[x], minus));
-                                if (masked && !((bits >> (e + x)) & 1)) q = 0.f;
-                                l += q;
-                                w[x] = E4M3 ? q * vv[x] : q;
-                                if (E4M3 && masked && !((bits >> (e + x)) & 1)) w[x] = 0.f;
-                            }
-                            p[e / 2] = pack_bf16(w[0], w[1]);
-                            p[e / 2 + 1] = pack_bf16(w[2], w[3]);
+                            p[e] = E4M3 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                            p[e + 1] = E4M3 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
                         }
-                        tmem_st16(s0 + c0 / 2, p);
+                        tmem_st16(s0 + (half * HC + c0) / 2, p);
                     }
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&B.pfull[st]);
+                if (lane == 0) mbar_arrive(&B.pfull[b]);
+                if (!busy && !ok) break;
             }
-            if (!ok) break;
             // ---- the segment's output
-            if (!warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) { ok = false; break; }
+            ok = ok && warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim);
+            if (busy ? pair_any(pair, !ok) : !ok) { ok = false; break; }
             tc_fence_after();
             const bool odd = !E4M3 && *reinterpret_cast<volatile int*>(&B.odd) != 0;
             if (busy) {
+                row_top[half * 128 + m] = l2.x + l2.y;
+                pair_sync(pair);
+                const float l = row_top[m] + row_top[128 + m];
                 const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
                 const bool empty = ref == kNegInf && l == 0.f;
                 const float inv = empty ? 0.f : 1.f / l;
                 const int64_t out = (t * a.H + head) * D;
                 float* part = partial_base(a) + (2 * (int64_t)blockIdx.x + seg.later) * slot_floats(D, a.slot_rows);
-                if (!whole && live) {
+                if (!whole && live && half == 0) {
                     part[m] = ref;
                     part[a.slot_rows + m] = l;
                 }
                 part += 2 * a.slot_rows + m * D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                     float o[32];
                     tmem_ld32(tmem + lane_off + c0, o);
                     tmem_wait_ld();
-                    if (E4M3) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {  // back to the elements' order
-                            const float x = o[e + 1];
-                            o[e + 1] = o[e + 2];
-                            o[e + 2] = x;
-                        }
-                    }
                     if (!live) continue;
                     if (odd) {
+                        // drafted values that are not finite, for the rows that see them
                         const int from = max(base, seg.tile0 * TN), to = min(seg.seq.len, seg.tile1 * TN);
                         for (int p = from; p < to; ++p) {
                             if (!((sees >> (p - base)) & 1)) continue;
@@ -595,8 +647,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
                                                 (vr + ((int64_t)seg.hk << a.c.page_shift)) * D + c0;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float x = bf16_to_f32(v[e]);
-                                if (!(fabsf(x) <= FLT_MAX)) o[e] += x;
+                                const float y = bf16_to_f32(v[e]);
+                                if (!(fabsf(y) <= FLT_MAX)) o[e] += y;
                             }
                         }
                     }
@@ -623,7 +675,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
                         *reinterpret_cast<uint4*>(y + e) = make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
                                                                      pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
                 }
-                if (whole && live && a.lse) a.lse[t * a.H + head] = empty ? kNegInf : ref * kLn2 + logf(l);
+                if (whole && live && half == 0 && a.lse)
+                    a.lse[t * a.H + head] = empty ? kNegInf : ref * kLn2 + logf(l);
+                pair_sync(pair);  // the sums are read
             }
             tc_fence_before();
             __syncwarp();
@@ -640,11 +694,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a) {
     }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// The cache's rows [n_pages * Hk * page, D] bf16; boxes of 64 elements x the
+// rows of a page that one tile can take, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* ptr, const CacheView& c, int rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)((c.n_pages * c.Hk) << c.page_shift)};
+    cuuint64_t strides[1] = {(cuuint64_t)c.D * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool E4M3>
 cudaError_t launch_tc(const TreeArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
+    using C = Tc<D, E4M3>;
+    CUtensorMap mk = {}, mv = {};
+    const int page = 1 << a.c.page_shift, run = page < C::TN ? page : C::TN;
+    if (!E4M3 && (!make_map(&mk, a.c.k, a.c, run) || !make_map(&mv, a.c.v, a.c, run))) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    tree_tc_kernel<D, E4M3><<<a.grid, kTcThreads, Tc<D>::kSmem, s>>>(a);
+    tree_tc_kernel<D, E4M3><<<a.grid, kTcThreads, C::kSmem, s>>>(a, mk, mv);
     return cudaGetLastError();
 }
 
