@@ -15,7 +15,10 @@
 //   warps 10-13  e4m3: raw tiles to f16 (exact) in the layout of the products;
 //                bf16: the tiles that hold drafted tokens or end the sequence,
 //                where rows past its end and drafted values that are not finite
-//                must be zero. Both: the queries
+//                must be zero
+// Queries and probabilities are the products' A operands in tensor memory, so
+// that shared memory -- written by the copies, read and written by the
+// conversion, read by the products -- carries only the tiles.
 // Tiles stand in one ring of slots in the order K0, V0, K1, V1, ..., so that the
 // keys of the next tiles do not wait for the values of this one.
 //
@@ -48,35 +51,35 @@ constexpr uint64_t kDrainWaitNs = 1000000000ull;
 template <int D, bool E4M3>
 struct Tc {
     static constexpr int TN = D == 256 ? 64 : 128;  // tokens of a tile
-    static constexpr int kBlockQ = kTcRows * 128;   // 64 elements of every row, 128-byte swizzled
-    static constexpr int kBlock = TN * 128;
+    static constexpr int kBlock = TN * 128;         // 64 elements of every row, 128-byte swizzled
     static constexpr int kBlocks = D / 64;
-    static constexpr int kQ = kBlockQ * kBlocks, kSlot = kBlock * kBlocks;
-    static constexpr int kSlots = E4M3 ? (D == 256 ? 3 : 4) : (D == 256 ? 5 : 6);
+    static constexpr int kSlot = kBlock * kBlocks;
+    static constexpr int kSlots = E4M3 ? 5 : 7;
     // raw e4m3 tiles: TN rows of D bytes, then TN scales
     static constexpr int kRaw = TN * D + TN * 4, kRawSlots = 3;
-    static constexpr int kOffSlots = kQ, kOffRaw = kOffSlots + kSlots * kSlot;
+    static constexpr int kOffRaw = kSlots * kSlot;
     static constexpr int kOffScale = kOffRaw + (E4M3 ? kRawSlots * kRaw : 0);  // [slot][k, v, log2 v][TN]
     static constexpr int kScaleBytes = E4M3 ? kScaleSlots * 3 * TN * 4 : 0;
-    static constexpr int kOffRows = kOffScale + kScaleBytes;      // maxima [2][128], row factors [2][128] (e4m3)
-    static constexpr int kOffBars = kOffRows + (E4M3 ? 4 : 2) * 128 * 4;
-    static constexpr int kUsed = kOffBars + 352 + 1024;           // 1024: alignment
+    static constexpr int kOffRows = kOffScale + kScaleBytes;      // what two warps tell each other: [2][128]
+    static constexpr int kOffBars = kOffRows + 2 * 128 * 4;
+    static constexpr int kUsed = kOffBars + 368 + 1024;           // 1024: alignment
     // above half of the SM's shared memory, so that a CTA has its tensor memory to itself
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
-    static constexpr int kColS = D == 256 ? 256 : 128;  // S buffers behind O
+    // tensor memory: O, the queries, two buffers of S
+    static constexpr int kColQ = D, kColS = D + D / 2;
     static constexpr uint32_t kFormat = E4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16 operands: format bits 0
     static constexpr uint32_t kIdescS = idesc_bf16(128, TN, 0, 0) & kFormat;
     static constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1) & kFormat;
 };
 
 struct TcBars {
-    uint64_t full[6], empty[6];      // slots of the products (4 converter warps, bf16: and the loader / commit)
+    uint64_t full[7], empty[7];      // slots of the products (4 converter warps, bf16: and the loader / commit)
     uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / 4 warps)
-    uint64_t hand[6];                // bf16: slot left to the converters (loader)
+    uint64_t hand[7];                // bf16: slot left to the converters (loader)
     uint64_t sfull[2], pfull[2];     // scores (commit), probabilities (8 warps)
     uint64_t odone, ofree;           // output product (commit), output read (8 warps)
-    uint64_t qfull, qempty;          // queries (4 warps / commit)
+    uint64_t qfull;                  // queries in tensor memory (8 warps)
     uint64_t cfull[kScaleSlots];     // a tile's scales (4 warps)
     uint64_t drain;
     uint32_t tmem;
@@ -84,7 +87,7 @@ struct TcBars {
     int odd;                         // some drafted value was not finite
     int gave_up[kSoftWarps];         // a softmax warp whose wait ran out, for its partner
 };
-static_assert(sizeof(TcBars) <= 352, "barrier block");
+static_assert(sizeof(TcBars) <= 368, "barrier block");
 
 __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     if (limit == 0) return mbar_test_wait(bar, parity);
@@ -164,14 +167,13 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     volatile int* abort_flag = &B.abort_flag;
     float* scales = reinterpret_cast<float*>(sm + C::kOffScale);
     float* row_top = reinterpret_cast<float*>(sm + C::kOffRows);  // [half][row]
-    float* row_mul = row_top + 256;                               // [segment parity][row] (e4m3)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.H / a.c.Hk;
     const uint64_t wlim = a.wait_ns;
     pdl_launch_dependents();
 
     if (tid == 0) {
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 7; ++i) {
             mbar_init(&B.full[i], E4M3 ? kConvWarps : kConvWarps + 1);
             mbar_init(&B.empty[i], 1);
             mbar_init(&B.hand[i], 1);
@@ -187,8 +189,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], kConvWarps);
         mbar_init(&B.odone, 1);
         mbar_init(&B.ofree, kSoftWarps);
-        mbar_init(&B.qfull, kConvWarps);
-        mbar_init(&B.qempty, 1);
+        mbar_init(&B.qfull, kSoftWarps);
         mbar_init(&B.drain, 1);
         fence_mbar_init();
         B.abort_flag = 0;
@@ -265,7 +266,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             }
                             continue;
                         }
-                        uint8_t* dst = sm + C::kOffSlots + st * C::kSlot + lane * run * 128;
+                        uint8_t* dst = sm + st * C::kSlot + lane * run * 128;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&B.full[st], C::kSlot);
                             mbar_arrive_n(&B.full[st], kConvWarps);
@@ -285,58 +286,27 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         if (!ok) fail();
         // no copy may land after the CTA is gone
         if (lane == 0)
-            for (int st = 0; st < 6; ++st)
+            for (int st = 0; st < 7; ++st)
                 if ((last_full >> st) & 1)
                     mbar_wait(E4M3 ? &B.rfull[st < 3 ? st : 0] : &B.full[st], (last_par >> st) & 1, kDrainWaitNs);
         __syncwarp();
     } else if (warp >= kConvWarp0) {
-        // ========================================== queries, conversion, last tiles
+        // =================================================== conversion, last tiles
         const int pt = tid - 32 * kConvWarp0;
-        int x = 0, seg_no = 0;
+        int x = 0;
         uint32_t hand_par = 0;  // per slot: phase of its next hand-over
         auto publish = [&](uint64_t* bar) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg), ++seg_no) {
-            if (seg_no > 0 && !warp_wait(&B.qempty, (seg_no - 1) & 1, abort_flag, wlim)) { ok = false; break; }
-            constexpr int kQPer = D / 8;  // 16-byte pieces of a query row: as many lanes
-#pragma unroll 2
-            for (int y = pt; y < kTcRows * kQPer; y += kConvThreads) {
-                const int m = y / kQPer, c8 = y % kQPer;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (m < seg.rows) {
-                    const int r = seg.rt * kTcRows + m;
-                    const int64_t t = seg.seq.first + r / G;
-                    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
-                                                       (int64_t)(seg.hk * G + r % G) * D + 8 * c8);
-                }
-                if (E4M3) {
-                    // to f16, the row scaled by a power of two that puts its largest element in [1, 2)
-                    uint32_t w[4] = {u.x, u.y, u.z, u.w}, top = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
-#pragma unroll
-                    for (int o = kQPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    uint32_t ex = top >> 7;  // a row that is not finite stays as it is
-                    ex = ex == 255u || top == 0u ? 127u : ex < 1u ? 1u : ex > 253u ? 253u : ex;
-                    const float down = __uint_as_float((254u - ex) << 23);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack_f16(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xFFFF0000u) * down);
-                    u = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (c8 == 0) row_mul[(seg_no & 1) * 128 + m] = __uint_as_float(ex << 23) * a.scale * kLog2e;
-                }
-                *reinterpret_cast<uint4*>(sm + (c8 >> 3) * C::kBlockQ + sw128_off(m, c8 & 7)) = u;
-            }
-            publish(&B.qfull);
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
             for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
                 const int left = seg.seq.len - tile * TN;  // tokens that exist, from the tile's first
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++x) {
                     const int st = x % C::kSlots;
-                    uint8_t* slot = sm + C::kOffSlots + st * C::kSlot;
+                    uint8_t* slot = sm + st * C::kSlot;
                     if (E4M3) {
                         const int rs = x % C::kRawSlots;
                         if (!warp_wait(&B.rfull[rs], (x / C::kRawSlots) & 1, abort_flag, wlim)) { ok = false; break; }
@@ -416,22 +386,25 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         // ================================================================ products
         if (lane == 0) {
             int i = 0, seg_no = 0;
-            auto scores = [&](int x, bool first, bool last, int sn) -> bool {  // S of tile x
+            // descriptors of the ring's first slot; a slot, a block or a k-step further is a
+            // constant added to the address field
+            const uint64_t kd = sw128_desc(smem_u32(sm), 16, 1024), vd = sw128_desc(smem_u32(sm), C::kBlock, 1024);
+            auto scores = [&](int x, bool first, int sn) -> bool {  // S of tile x
                 const int g = 2 * x, st = g % C::kSlots, b = x & 1;
                 if (first && !tc_wait(&B.qfull, sn & 1, abort_flag, wlim)) return false;
                 if (!tc_wait(&B.full[st], (g / C::kSlots) & 1, abort_flag, wlim)) return false;
                 tc_fence_after();
-                const uint32_t k0 = smem_u32(sm + C::kOffSlots + st * C::kSlot), q0 = smem_u32(sm);
-#pragma unroll 4
+                const uint64_t d0 = kd + (uint64_t)(st * (C::kSlot >> 4));
+                const uint32_t s0 = tmem + C::kColS + b * TN;
+#pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tmem + C::kColS + b * TN, sw128_desc(q0 + (kk >> 2) * C::kBlockQ + 32 * (kk & 3), 16, 1024),
-                             sw128_desc(k0 + (kk >> 2) * C::kBlock + 32 * (kk & 3), 16, 1024), C::kIdescS, kk > 0);
+                    mma_bf16_ta(s0, tmem + C::kColQ + 8 * kk, d0 + (((kk >> 2) * C::kBlock + 32 * (kk & 3)) >> 4), C::kIdescS,
+                                kk > 0);
                 mma_commit(&B.sfull[b]);
                 mma_commit(&B.empty[st]);
-                if (last) mma_commit(&B.qempty);
                 return true;
             };
-            if (have) ok = scores(0, true, seg.tile1 - seg.tile0 == 1, 0);
+            if (have) ok = scores(0, true, 0);
             int tile = have ? seg.tile0 : 0;
             while (ok && have) {
                 Segment next = seg;
@@ -442,7 +415,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     more = next_segment<kTcRows, TN>(a, share, next);
                     next_tile = next.tile0;
                 }
-                if (!crosses && !scores(i + 1, false, next_tile + 1 == seg.tile1, seg_no)) { ok = false; break; }
+                if (!crosses && !scores(i + 1, false, seg_no)) { ok = false; break; }
                 const int g = 2 * i + 1, st = g % C::kSlots, b = i & 1;
                 if ((tile == seg.tile0 && seg_no > 0 && !tc_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim)) ||
                     !tc_wait(&B.pfull[b], (i >> 1) & 1, abort_flag, wlim) ||
@@ -451,16 +424,16 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     break;
                 }
                 tc_fence_after();
-                const uint32_t v0 = smem_u32(sm + C::kOffSlots + st * C::kSlot);
-#pragma unroll 4
+                const uint64_t d0 = vd + (uint64_t)(st * (C::kSlot >> 4));
+                const uint32_t p0 = tmem + C::kColS + b * TN;
+#pragma unroll
                 for (int kk = 0; kk < TN / 16; ++kk)
-                    mma_bf16_ta(tmem, tmem + C::kColS + b * TN + 8 * kk, sw128_desc(v0 + 2048 * kk, C::kBlock, 1024),
-                                C::kIdescO, tile != seg.tile0 || kk > 0);
+                    mma_bf16_ta(tmem, p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO, tile != seg.tile0 || kk > 0);
                 mma_commit(&B.odone);
                 mma_commit(&B.empty[st]);
                 if (crosses && more) {
                     ++seg_no;
-                    if (!scores(i + 1, true, next.tile1 - next.tile0 == 1, seg_no)) { ok = false; break; }
+                    if (!scores(i + 1, true, seg_no)) { ok = false; break; }
                 }
                 ++i;
                 seg = next;
@@ -479,8 +452,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         const int m = 32 * quarter + lane;  // row of the tile, lane of tensor memory
         const int pair = 1 + quarter;       // named barrier of the two warps
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-        int i = 0, seg_no = 0;
-        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg), ++seg_no) {
+        int i = 0;
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
             const bool busy = 32 * quarter < seg.rows, live = m < seg.rows;
             const int r = seg.rt * kTcRows + (live ? m : 0);
             const int node = r / G, head = seg.hk * G + r % G;
@@ -493,6 +466,51 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             }
             float ref = kNegInf, mul = a.scale * kLog2e;
             float2 l2 = make_float2(0.f, 0.f);
+            // ---- queries to tensor memory: half of the row per warp (the products that read
+            // the last segment's are done: their scores have been here)
+            if (busy) {
+                const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
+                                                                 (int64_t)head * D + half * (D / 2));
+                float down = 1.f;
+                if (E4M3) {
+                    // as f16, the row scaled by a power of two that puts its largest element in [1, 2)
+                    uint32_t big = 0;
+#pragma unroll 4
+                    for (int e = 0; e < D / 16; ++e) {
+                        const uint4 u = live ? qp[e] : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) big = max(big, max(w[y] & 0x7FFFu, w[y] >> 16 & 0x7FFFu));
+                    }
+                    row_top[half * 128 + m] = __uint_as_float(big);
+                    pair_sync(pair);
+                    big = max(big, __float_as_uint(row_top[(half ^ 1) * 128 + m]));
+                    uint32_t ex = big >> 7;  // a row that is not finite stays as it is
+                    ex = ex == 255u || big == 0u ? 127u : ex < 1u ? 1u : ex > 253u ? 253u : ex;
+                    down = __uint_as_float((254u - ex) << 23);
+                    mul *= __uint_as_float(ex << 23);
+                }
+#pragma unroll 1
+                for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 u = live ? qp[c0 / 8 + e] : make_uint4(0, 0, 0, 0);
+                        w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
+                    }
+                    if (E4M3) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack_f16(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xFFFF0000u) * down);
+                    }
+                    tmem_st16(tmem + lane_off + C::kColQ + half * (D / 4) + c0 / 2, w);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.qfull);
+            if (E4M3 && busy) pair_sync(pair);  // (what the warps told each other is read)
             for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++i) {
                 const int b = i & 1;
                 // A warp whose wait runs out goes on to the vote below, where its partner
@@ -501,7 +519,6 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                      (!E4M3 || warp_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim)) && ok;
                 tc_fence_after();
                 if (busy) {
-                    if (E4M3 && tile == seg.tile0) mul = live ? row_mul[(seg_no & 1) * 128 + m] : 0.f;
                     const uint32_t s0 = tmem + lane_off + C::kColS + b * TN;
                     const float* sc = scales + (i % kScaleSlots) * 3 * TN + half * HC;
                     const int off = tile * TN + half * HC - base;  // this half's start past the context
