@@ -99,6 +99,16 @@ __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile in
         if (*abort_flag || globaltimer_ns() - t0 > limit) return false;
     }
 }
+// All lanes of a warp wait alike; the first probe is inline.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, limit));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
+    return y != 0;
+}
 // The same for a whole warp: one lane waits, all of them learn the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     const bool ok = (threadIdx.x & 31) != 0 || tc_wait(bar, parity, abort_flag, limit);
@@ -167,7 +177,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     volatile int* abort_flag = &B.abort_flag;
     float* scales = reinterpret_cast<float*>(sm + C::kOffScale);
     float* row_top = reinterpret_cast<float*>(sm + C::kOffRows);  // [half][row]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (warp-uniform to the compiler)
     const int G = a.H / a.c.Hk;
     const uint64_t wlim = a.wait_ns;
     pdl_launch_dependents();
@@ -384,67 +395,71 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         if (!ok) fail();
     } else if (warp == kMmaWarp) {
         // ================================================================ products
-        if (lane == 0) {
-            int i = 0, seg_no = 0;
-            // descriptors of the ring's first slot; a slot, a block or a k-step further is a
-            // constant added to the address field
-            const uint64_t kd = sw128_desc(smem_u32(sm), 16, 1024), vd = sw128_desc(smem_u32(sm), C::kBlock, 1024);
-            auto scores = [&](int x, bool first, int sn) -> bool {  // S of tile x
-                const int g = 2 * x, st = g % C::kSlots, b = x & 1;
-                if (first && !tc_wait(&B.qfull, sn & 1, abort_flag, wlim)) return false;
-                if (!tc_wait(&B.full[st], (g / C::kSlots) & 1, abort_flag, wlim)) return false;
-                tc_fence_after();
-                const uint64_t d0 = kd + (uint64_t)(st * (C::kSlot >> 4));
-                const uint32_t s0 = tmem + C::kColS + b * TN;
+        // The whole warp walks the tiles alike and one elected lane issues: the
+        // descriptors are then warp-uniform values.
+        // Descriptors of the ring's first slot; a slot, a block or a k-step further
+        // is a constant added to the address field.
+        const uint64_t kd = sw128_desc(smem_u32(sm), 16, 1024), vd = sw128_desc(smem_u32(sm), C::kBlock, 1024);
+        int ks = 0, vs = 1, kpar = 0, vpar = 0;  // slots of the next keys and values, their phases
+        auto advance = [](int& st, int& par) {   // two groups further
+            st += 2;
+            if (st >= C::kSlots) {
+                st -= C::kSlots;
+                par ^= 1;
+            }
+        };
+        auto scores = [&](int b) -> bool {  // S of the next tile into buffer b
+            if (!all_wait(&B.full[ks], kpar, abort_flag, wlim)) return false;
+            tc_fence_after();
+            const uint64_t d0 = kd + (uint64_t)(ks * (C::kSlot >> 4));
+            const uint32_t s0 = tmem + C::kColS + b * TN;
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_bf16_ta(s0, tmem + C::kColQ + 8 * kk, d0 + (((kk >> 2) * C::kBlock + 32 * (kk & 3)) >> 4), C::kIdescS,
                                 kk > 0);
                 mma_commit(&B.sfull[b]);
-                mma_commit(&B.empty[st]);
-                return true;
-            };
-            if (have) ok = scores(0, true, 0);
-            int tile = have ? seg.tile0 : 0;
-            while (ok && have) {
-                Segment next = seg;
-                int next_tile = tile + 1;
-                const bool crosses = next_tile == seg.tile1;
-                bool more = true;
-                if (crosses) {
-                    more = next_segment<kTcRows, TN>(a, share, next);
-                    next_tile = next.tile0;
-                }
-                if (!crosses && !scores(i + 1, false, seg_no)) { ok = false; break; }
-                const int g = 2 * i + 1, st = g % C::kSlots, b = i & 1;
-                if ((tile == seg.tile0 && seg_no > 0 && !tc_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim)) ||
-                    !tc_wait(&B.pfull[b], (i >> 1) & 1, abort_flag, wlim) ||
-                    !tc_wait(&B.full[st], (g / C::kSlots) & 1, abort_flag, wlim)) {
+                mma_commit(&B.empty[ks]);
+            }
+            __syncwarp();
+            advance(ks, kpar);
+            return true;
+        };
+        int b = 0, ppar = 0;
+        if (have) ok = all_wait(&B.qfull, 0, abort_flag, wlim) && scores(0);
+        for (int seg_no = 0; ok && have; ++seg_no) {
+            const int tiles = seg.tile1 - seg.tile0;
+            const bool more = next_segment<kTcRows, TN>(a, share, seg);
+            if (seg_no > 0) ok = all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim);
+            for (int y = 0; ok && y < tiles; ++y) {
+                // the next scores first: of this segment, or (below) of the next one
+                if (y + 1 < tiles && !scores(b ^ 1)) { ok = false; break; }
+                if (!all_wait(&B.full[vs], vpar, abort_flag, wlim) || !all_wait(&B.pfull[b], ppar, abort_flag, wlim)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t d0 = vd + (uint64_t)(st * (C::kSlot >> 4));
+                const uint64_t d0 = vd + (uint64_t)(vs * (C::kSlot >> 4));
                 const uint32_t p0 = tmem + C::kColS + b * TN;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < TN / 16; ++kk)
-                    mma_bf16_ta(tmem, p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO, tile != seg.tile0 || kk > 0);
-                mma_commit(&B.odone);
-                mma_commit(&B.empty[st]);
-                if (crosses && more) {
-                    ++seg_no;
-                    if (!scores(i + 1, true, seg_no)) { ok = false; break; }
+                    for (int kk = 0; kk < TN / 16; ++kk)
+                        mma_bf16_ta(tmem, p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO, y > 0 || kk > 0);
+                    mma_commit(&B.odone);
+                    mma_commit(&B.empty[vs]);
                 }
-                ++i;
-                seg = next;
-                tile = next_tile;
-                have = more;
+                __syncwarp();
+                advance(vs, vpar);
+                b ^= 1;
+                if (b == 0) ppar ^= 1;
             }
-            if (!ok) fail();
-            mma_commit(&B.drain);
-            mbar_wait(&B.drain, 0, kDrainWaitNs);
+            if (ok && more) ok = all_wait(&B.qfull, (seg_no + 1) & 1, abort_flag, wlim) && scores(b);
+            have = more;
         }
+        if (!ok && lane == 0) fail();
+        if (elect_one()) mma_commit(&B.drain);
         __syncwarp();
+        mbar_wait(&B.drain, 0, kDrainWaitNs);
     } else {
         // ================================================================= softmax
         constexpr int HC = TN / 2;  // tokens of this warp's half
