@@ -109,12 +109,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
     return y != 0;
 }
-// The same for a whole warp: one lane waits, all of them learn the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
-    const bool ok = (threadIdx.x & 31) != 0 || tc_wait(bar, parity, abort_flag, limit);
-    return __all_sync(0xffffffffu, ok);
-}
-
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
@@ -255,7 +249,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 for (int kv = 0; kv < 2; ++kv, ++x) {
                     if (E4M3) {
                         const int st = x % C::kRawSlots, use = x / C::kRawSlots;
-                        if (!warp_wait(&B.rempty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        if (!all_wait(&B.rempty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
                         uint8_t* dst = sm + C::kOffRaw + st * C::kRaw;
                         if (lane == 0) mbar_arrive_expect_tx(&B.rfull[st], (uint32_t)(n_runs * run * (D + 4)));
                         last_full |= 1u << st;
@@ -269,7 +263,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         }
                     } else {
                         const int st = x % C::kSlots, use = x / C::kSlots;
-                        if (!warp_wait(&B.empty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        if (!all_wait(&B.empty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
                         if (by_hand(seg, tile)) {  // (the converters walk only these: a slot's phases are followed here)
                             if (lane == 0) {
                                 mbar_arrive(&B.full[st]);
@@ -320,7 +314,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     uint8_t* slot = sm + st * C::kSlot;
                     if (E4M3) {
                         const int rs = x % C::kRawSlots;
-                        if (!warp_wait(&B.rfull[rs], (x / C::kRawSlots) & 1, abort_flag, wlim)) { ok = false; break; }
+                        if (!all_wait(&B.rfull[rs], (x / C::kRawSlots) & 1, abort_flag, wlim)) { ok = false; break; }
                         const uint8_t* raw = sm + C::kOffRaw + rs * C::kRaw;
                         if (pt < TN) {
                             const float s = reinterpret_cast<const float*>(raw + TN * D)[pt];
@@ -332,37 +326,45 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&B.cfull[(x >> 1) % kScaleSlots]);
                         }
-                        if (!warp_wait(&B.empty[st], ((x / C::kSlots) & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
-                        constexpr int kPer = D / 16, kPieces = TN * kPer / kConvThreads, kAhead = 4;
-                        const int col = pt % kPer, tok0 = pt / kPer;
-                        // neighbouring blocks start with the other half: eight lanes, eight bank groups
-                        const int f = (col >> 2) & 1, c16 = 2 * (col & 3);
-#pragma unroll 1
-                        for (int j0 = 0; j0 < kPieces; j0 += kAhead) {
-                            uint4 u[kAhead];
+                        if (!all_wait(&B.empty[st], ((x / C::kSlots) & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                        // A lane takes 16-byte pieces of every second token: piece col of block
+                        // y ^ h, h the token's parity. Eight lanes then read 64 bytes each of
+                        // two rows, in different bank groups, and write two rows of two blocks
+                        // whose swizzles fall into different bank groups as well.
+                        const int col = lane & 3, h = (lane >> 2) & 1;
+                        const int tok0 = 8 * (warp - kConvWarp0) + 2 * (lane >> 3) + h;
+                        const uint8_t* in = raw + tok0 * D + 16 * col;
+                        uint8_t* out0 = slot + sw128_off(tok0, 2 * col);
+                        uint8_t* out1 = slot + sw128_off(tok0, 2 * col + 1);
+                        const bool whole = left >= TN;
 #pragma unroll
-                            for (int j = 0; j < kAhead; ++j) {
-                                const int tok = tok0 + (j0 + j) * (kConvThreads / kPer);
-                                u[j] = *reinterpret_cast<const uint4*>(raw + tok * D + 16 * col);
-                                if (tok >= left) u[j] = make_uint4(0, 0, 0, 0);
-                            }
+                        for (int y = 0; y < C::kBlocks; ++y) {
+                            const int block = C::kBlocks > 1 ? y ^ h : 0;
 #pragma unroll
-                            for (int j = 0; j < kAhead; ++j) {
-                                const int tok = tok0 + (j0 + j) * (kConvThreads / kPer);
-                                const uint4 lo = make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
-                                                            e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
-                                const uint4 hi = make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
-                                                            e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
-                                uint8_t* p = slot + (col >> 2) * C::kBlock;
-                                *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + f)) = f ? hi : lo;
-                                *reinterpret_cast<uint4*>(p + sw128_off(tok, c16 + 1 - f)) = f ? lo : hi;
+                            for (int j0 = 0; j0 < TN; j0 += 64) {
+                                uint4 u[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    u[j] = *reinterpret_cast<const uint4*>(in + (j0 + 32 * j) * D + 64 * block);
+                                    if (!whole && tok0 + j0 + 32 * j >= left) u[j] = make_uint4(0, 0, 0, 0);
+                                }
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int at = block * C::kBlock + (j0 + 32 * j) * 128;
+                                    *reinterpret_cast<uint4*>(out0 + at) =
+                                        make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
+                                                   e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
+                                    *reinterpret_cast<uint4*>(out1 + at) =
+                                        make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
+                                                   e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
+                                }
                             }
                         }
                         publish(&B.full[st]);
                         if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
                     } else {
                         if (!by_hand(seg, tile)) continue;
-                        if (!warp_wait(&B.hand[st], (hand_par >> st) & 1, abort_flag, wlim)) { ok = false; break; }
+                        if (!all_wait(&B.hand[st], (hand_par >> st) & 1, abort_flag, wlim)) { ok = false; break; }
                         hand_par ^= 1u << st;
                         constexpr int kPer = D / 8;
                         const int draft = seg.seq.len - seg.seq.nodes - tile * TN;  // the draft's first token here
@@ -530,8 +532,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 const int b = i & 1;
                 // A warp whose wait runs out goes on to the vote below, where its partner
                 // learns of it: neither may stay alone at their barrier.
-                ok = warp_wait(&B.sfull[b], (i >> 1) & 1, abort_flag, wlim) &&
-                     (!E4M3 || warp_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim)) && ok;
+                ok = all_wait(&B.sfull[b], (i >> 1) & 1, abort_flag, wlim) &&
+                     (!E4M3 || all_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim)) && ok;
                 tc_fence_after();
                 if (busy) {
                     const uint32_t s0 = tmem + lane_off + C::kColS + b * TN;
@@ -593,7 +595,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         if (move) ref = top;
                         l2 = mul2(l2, make_float2(f, f));
                         if (tile != seg.tile0) {
-                            if (!warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) ok = false;
+                            if (!all_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) ok = false;
                             tc_fence_after();
 #pragma unroll 1
                             for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
@@ -644,7 +646,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 if (!busy && !ok) break;
             }
             // ---- the segment's output
-            ok = ok && warp_wait(&B.odone, (i - 1) & 1, abort_flag, wlim);
+            ok = ok && all_wait(&B.odone, (i - 1) & 1, abort_flag, wlim);
             if (busy ? pair_any(pair, !ok) : !ok) { ok = false; break; }
             tc_fence_after();
             const bool odd = !E4M3 && *reinterpret_cast<volatile int*>(&B.odd) != 0;
