@@ -628,7 +628,7 @@ cudaError_t launch_config(const TreeArgs& a, bool tc, cudaStream_t s) {
     const dim3 join(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps);
     const cudaError_t e = tc ? launch_tree_tc(a, s) : rows <= 8 ? launch_mma<D, E4M3, 1>(a, s) : launch_mma<D, E4M3, 2>(a, s);
     if (e != cudaSuccess) return e;
-    if (tc) return launch_pdl(join_kernel<D, kTcRows, (D == 256 ? 64 : 128)>, join, dim3(kThreads), 0, s, a);
+    if (tc) return launch_pdl(join_kernel<D, kTcRows, kTcTile>, join, dim3(kThreads), 0, s, a);
     return launch_pdl(join_kernel<D, kRows, kTile>, join, dim3(kThreads), 0, s, a);
 }
 

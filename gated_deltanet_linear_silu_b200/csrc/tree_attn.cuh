@@ -18,6 +18,7 @@
 namespace gdn {
 
 constexpr int kTcRows = 128;    // query rows of a row tile (tcgen05 kernel)
+constexpr int kTcTile = 64;     // tokens of its tiles
 constexpr int kMaxRowTiles = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

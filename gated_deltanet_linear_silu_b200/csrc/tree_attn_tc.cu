@@ -4,27 +4,30 @@
 // A unit is (sequence, key/value head, 128 query rows), rows the M side of the
 // products. One persistent CTA per SM walks an equal share of its row tile's
 // line in tiles of TN tokens; 14 warps:
-//   warps 0-7    softmax: two warps per 32 rows, half of the tile's tokens each,
-//                a row per thread; probabilities back to tensor memory; the
-//                output at the end of a segment
+//   warps 0-7    softmax, a row per thread, four warps to a tile: even tiles and
+//                odd tiles have their own running state and output accumulator
+//                (D <= 128), so that one group's exponentials run beside the
+//                other's maxima and neither waits for it. For D = 256 the two
+//                accumulators do not fit: two warps share 32 rows and take half
+//                of every tile each. Probabilities go back to tensor memory
 //   warp 8       issues the products: S = Q K^T of tile i + 1 goes out before
-//                O += P V of tile i, so that the next scores form meanwhile
+//                O += P V of tile i
 //   warp 9       loader: the tile's pages, a lane per page. bf16 tiles go
 //                straight to their slots by TMA (128-byte swizzle); e4m3 pages
 //                by bulk copies into a raw ring
-//   warps 10-13  e4m3: raw tiles to f16 (exact) in the layout of the products;
-//                bf16: the tiles that hold drafted tokens or end the sequence,
-//                where rows past its end and drafted values that are not finite
-//                must be zero
-// Queries and probabilities are the products' A operands in tensor memory, so
-// that shared memory -- written by the copies, read and written by the
-// conversion, read by the products -- carries only the tiles.
+//   from 10      converters. e4m3: raw tiles to f16 (exact) in the layout of the
+//                products; bf16: the tiles that hold drafted tokens or end the
+//                sequence, where rows past its end and drafted values that are
+//                not finite must be zero
+// Probabilities (and queries, where tensor memory has room) are the products' A
+// operands in tensor memory: shared memory carries the copies, the conversion
+// and the products' other operand, and is the next limit.
 // Tiles stand in one ring of slots in the order K0, V0, K1, V1, ..., so that the
 // keys of the next tiles do not wait for the values of this one.
 //
-// Scales, f16 and the reference R are those of tree_attn.cu. Two warps share a
-// row's reference: they vote at a named barrier on whether it has to move, and
-// only then exchange maxima and rescale the output in tensor memory.
+// Scales, f16 and the reference R are those of tree_attn.cu. Where two warps
+// share a row's reference (D = 256) they vote at a named barrier on whether it
+// has to move, and only then exchange maxima and rescale the output.
 //
 // Every wait is bounded (gdn_set_wait_limit_ns).
 #include <cuda.h>
@@ -43,51 +46,58 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kConvWarp0 = 10, kConvWarps = 4;
-constexpr int kTcThreads = 32 * (kConvWarp0 + kConvWarps), kConvThreads = 32 * kConvWarps;
-constexpr int kScaleSlots = 4;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kConvWarp0 = 10;
+constexpr int kScaleSlots = 8;  // (at least a tile's lead over the softmax, in tiles)
 constexpr uint64_t kDrainWaitNs = 1000000000ull;
+
+constexpr int TN = kTcTile;
 
 template <int D, bool E4M3>
 struct Tc {
-    static constexpr int TN = D == 256 ? 64 : 128;  // tokens of a tile
-    static constexpr int kBlock = TN * 128;         // 64 elements of every row, 128-byte swizzled
+    static constexpr bool kGroups = D <= 128;  // even and odd tiles apart
+    // bf16 needs few converters, and 12 warps leave 168 registers to a thread
+    static constexpr int kConvWarps = E4M3 ? 4 : 2;
+    static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
+    static constexpr int kBlock = TN * 128;  // 64 elements of every row, 128-byte swizzled
     static constexpr int kBlocks = D / 64;
     static constexpr int kSlot = kBlock * kBlocks;
-    static constexpr int kSlots = E4M3 ? 5 : 7;
+    static constexpr int kSlots = D == 256 ? (E4M3 ? 4 : 6) : (E4M3 ? 8 : 12);  // (even: two to a tile)
     // raw e4m3 tiles: TN rows of D bytes, then TN scales
-    static constexpr int kRaw = TN * D + TN * 4, kRawSlots = 3;
+    static constexpr int kRaw = TN * D + TN * 4, kRawSlots = E4M3 ? (D == 256 ? 4 : 6) : 1;
     static constexpr int kOffRaw = kSlots * kSlot;
     static constexpr int kOffScale = kOffRaw + (E4M3 ? kRawSlots * kRaw : 0);  // [slot][k, v, log2 v][TN]
     static constexpr int kScaleBytes = E4M3 ? kScaleSlots * 3 * TN * 4 : 0;
-    static constexpr int kOffRows = kOffScale + kScaleBytes;      // what two warps tell each other: [2][128]
-    static constexpr int kOffBars = kOffRows + 2 * 128 * 4;
-    static constexpr int kUsed = kOffBars + 368 + 1024;           // 1024: alignment
+    static constexpr int kOffRows = kOffScale + kScaleBytes;  // what two warps tell each other: [2][2][128]
+    static constexpr int kOffBars = kOffRows + 4 * 128 * 4;
+    static constexpr int kUsed = kOffBars + 704 + 1024;       // 1024: alignment
     // above half of the SM's shared memory, so that a CTA has its tensor memory to itself
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
-    // tensor memory: O, the queries, two buffers of S
-    static constexpr int kColQ = D, kColS = D + D / 2;
+    // tensor memory: O (one or two), the queries, two or three buffers of S
+    static constexpr int kBufs = kGroups ? 3 : 2;
+    static constexpr int kColQ = kGroups ? 2 * D : D, kColS = kColQ + D / 2;
+    static_assert(kColS + kBufs * TN <= 512, "tensor memory");
     static constexpr uint32_t kFormat = E4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16 operands: format bits 0
     static constexpr uint32_t kIdescS = idesc_bf16(128, TN, 0, 0) & kFormat;
     static constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1) & kFormat;
 };
 
 struct TcBars {
-    uint64_t full[7], empty[7];      // slots of the products (4 converter warps, bf16: and the loader / commit)
-    uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / 4 warps)
-    uint64_t hand[7];                // bf16: slot left to the converters (loader)
-    uint64_t sfull[2], pfull[2];     // scores (commit), probabilities (8 warps)
-    uint64_t odone, ofree;           // output product (commit), output read (8 warps)
+    uint64_t full[12], empty[12];    // slots of the products (converter warps; bf16: loader, or one of them / commit)
+    uint64_t hand[12];               // bf16: slot left to the converters (loader)
+    uint64_t rfull[6], rempty[6];    // raw slots (bulk copies / converter warps)
+    uint64_t cfull[kScaleSlots];     // a tile's scales (converter warps)
+    uint64_t sfull[3], pfull[3];     // scores (commit), probabilities (4 or 8 warps)
+    uint64_t odone[2];               // output product of a tile done, per accumulator (commit)
+    uint64_t oend, ofree;            // of a segment: all of them done (commit), output read (8 warps)
     uint64_t qfull;                  // queries in tensor memory (8 warps)
-    uint64_t cfull[kScaleSlots];     // a tile's scales (4 warps)
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
     int odd;                         // some drafted value was not finite
     int gave_up[kSoftWarps];         // a softmax warp whose wait ran out, for its partner
 };
-static_assert(sizeof(TcBars) <= 368, "barrier block");
+static_assert(sizeof(TcBars) <= 704, "barrier block");
 
 __device__ __noinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
     if (limit == 0) return mbar_test_wait(bar, parity);
@@ -109,10 +119,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
     return y != 0;
 }
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
-
 // The 64 softmax threads of two warps with the same rows, at their named barrier.
 __device__ __forceinline__ bool pair_any(int id, bool x) {
     uint32_t y;
@@ -137,6 +143,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
     return *reinterpret_cast<float2*>(&y);
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(y)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&y);
+}
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -151,26 +168,19 @@ __device__ __forceinline__ uint32_t sees32(uint64_t sees, int off) {
     return (uint32_t)(sees << -off) | ((1u << -off) - 1u);
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
-
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__((Tc<D, E4M3>::kThreads), 1)
 tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v) {
     using C = Tc<D, E4M3>;
-    constexpr int TN = C::TN;
+    constexpr int kConvWarps = C::kConvWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     TcBars& B = *reinterpret_cast<TcBars*>(sm + C::kOffBars);
     volatile int* abort_flag = &B.abort_flag;
     float* scales = reinterpret_cast<float*>(sm + C::kOffScale);
-    float* row_top = reinterpret_cast<float*>(sm + C::kOffRows);  // [half][row]
+    float* row_top = reinterpret_cast<float*>(sm + C::kOffRows);  // [half or group][row]
+    float* row_sum = row_top + 256;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (warp-uniform to the compiler)
     const int G = a.H / a.c.Hk;
@@ -178,21 +188,23 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     pdl_launch_dependents();
 
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) {
-            mbar_init(&B.full[i], E4M3 ? kConvWarps : kConvWarps + 1);
+        for (int i = 0; i < 12; ++i) {
+            mbar_init(&B.full[i], E4M3 ? kConvWarps : 1);
             mbar_init(&B.empty[i], 1);
             mbar_init(&B.hand[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 6; ++i) {
             mbar_init(&B.rfull[i], 1);
             mbar_init(&B.rempty[i], kConvWarps);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&B.sfull[i], 1);
-            mbar_init(&B.pfull[i], kSoftWarps);
-        }
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], kConvWarps);
-        mbar_init(&B.odone, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&B.sfull[i], 1);
+            mbar_init(&B.pfull[i], C::kGroups ? kSoftWarps / 2 : kSoftWarps);
+        }
+        mbar_init(&B.odone[0], 1);
+        mbar_init(&B.odone[1], 1);
+        mbar_init(&B.oend, 1);
         mbar_init(&B.ofree, kSoftWarps);
         mbar_init(&B.qfull, kSoftWarps);
         mbar_init(&B.drain, 1);
@@ -203,7 +215,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     }
     if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
     tc_fence_before();
-    const Share share = find_share<kTcRows, TN, kTcThreads>(a);  // (synchronises the CTA)
+    const Share share = find_share<kTcRows, TN, C::kThreads>(a);  // (synchronises the CTA)
     tc_fence_after();
     const uint32_t tmem = B.tmem;
     auto fail = [&]() {
@@ -228,62 +240,73 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             prefetch_tmap(&map_k);
             prefetch_tmap(&map_v);
         }
-        int x = 0;                               // group: tile x / 2's keys (even) or values
         uint32_t last_full = 0, last_par = 0;    // copies in flight, for the end
+        int rst = 0, rpar = 1;                   // raw slot, phase of its last release
+        int st = 0, par = 1;                     // slot, likewise
         for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
+            // This lane's page of a tile (every lane's, where a page holds a tile). The
+            // table is read one tile ahead, and what is read is not looked at before
+            // its tile comes.
+            const int at = run == TN ? 0 : lane;
+            auto page_id = [&](int tile) -> int {
+                const int pos = tile * TN + at * run;
+                return tile < seg.tile1 && at < TN / run && pos < seg.seq.len
+                           ? __ldg(a.p.table + (int64_t)seg.n * a.p.max_pages + (pos >> a.c.page_shift))
+                           : 0;
+            };
+            int next_id = page_id(seg.tile0);
             for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
-                // this lane's page of the tile
-                const int pos = tile * TN + lane * run;
                 const int n_runs = min(TN / run, (min(TN, seg.seq.len - tile * TN) + run - 1) / run);
-                int row = 0;
-                if (lane < n_runs) {
-                    row = (int)page_row(a.p, a.c, seg.n, pos);
-                    if (row < 0) {
-                        set_status(a.status, kStatusBadSeqlens);
-                        row = 0;  // some rows of the pool: the sequence's output means nothing
-                    } else {
-                        row += seg.hk << a.c.page_shift;
-                    }
+                int id = next_id;
+                next_id = page_id(tile + 1);
+                if (id < 0 || id >= a.c.n_pages) {
+                    set_status(a.status, kStatusBadSeqlens);
+                    id = 0;  // some rows of the pool: the sequence's output means nothing
                 }
+                const int row = ((id * a.c.Hk + seg.hk) << a.c.page_shift) + ((tile * TN + at * run) & (page - 1));
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++x) {
+                for (int kv = 0; kv < 2; ++kv) {
                     if (E4M3) {
-                        const int st = x % C::kRawSlots, use = x / C::kRawSlots;
-                        if (!all_wait(&B.rempty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
-                        uint8_t* dst = sm + C::kOffRaw + st * C::kRaw;
-                        if (lane == 0) mbar_arrive_expect_tx(&B.rfull[st], (uint32_t)(n_runs * run * (D + 4)));
-                        last_full |= 1u << st;
-                        last_par = (last_par & ~(1u << st)) | (uint32_t)(use & 1) << st;
+                        if (!all_wait(&B.rempty[rst], rpar, abort_flag, wlim)) { ok = false; break; }
+                        uint8_t* dst = sm + C::kOffRaw + rst * C::kRaw;
+                        if (lane == 0) mbar_arrive_expect_tx(&B.rfull[rst], (uint32_t)(n_runs * run * (D + 4)));
+                        last_full |= 1u << rst;
+                        last_par = (last_par & ~(1u << rst)) | (uint32_t)(rpar ^ 1) << rst;
                         __syncwarp();
                         if (lane < n_runs) {
                             bulk_load(dst + lane * run * D, static_cast<const uint8_t*>(kv ? a.c.v : a.c.k) + (int64_t)row * D,
-                                      run * D, &B.rfull[st]);
+                                      run * D, &B.rfull[rst]);
                             bulk_load(dst + TN * D + lane * run * 4, (kv ? a.c.v_scale : a.c.k_scale) + row, run * 4,
-                                      &B.rfull[st]);
+                                      &B.rfull[rst]);
                         }
-                    } else {
-                        const int st = x % C::kSlots, use = x / C::kSlots;
-                        if (!all_wait(&B.empty[st], (use & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
-                        if (by_hand(seg, tile)) {  // (the converters walk only these: a slot's phases are followed here)
-                            if (lane == 0) {
-                                mbar_arrive(&B.full[st]);
-                                mbar_arrive(&B.hand[st]);
-                            }
-                            continue;
-                        }
-                        uint8_t* dst = sm + st * C::kSlot + lane * run * 128;
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&B.full[st], C::kSlot);
-                            mbar_arrive_n(&B.full[st], kConvWarps);
-                        }
-                        last_full |= 1u << st;
-                        last_par = (last_par & ~(1u << st)) | (uint32_t)(use & 1) << st;
                         __syncwarp();
-                        if (lane < n_runs) {
+                        if (++rst == C::kRawSlots) rst = 0, rpar ^= 1;
+                    } else {
+                        if (!all_wait(&B.empty[st], par, abort_flag, wlim)) { ok = false; break; }
+                        if (by_hand(seg, tile)) {  // (the converters walk only these: a slot's phases are followed here)
+                            if (lane == 0) mbar_arrive(&B.hand[st]);
+                        } else {
+                            uint8_t* dst = sm + st * C::kSlot;
+                            last_full |= 1u << st;
+                            last_par = (last_par & ~(1u << st)) | (uint32_t)(par ^ 1) << st;
+                            if (run == TN) {
+                                if (elect_one()) {
+                                    mbar_arrive_expect_tx(&B.full[st], C::kSlot);
+                                    tma_load_3d(dst, kv ? &map_v : &map_k, &B.full[st], 0, row, 0);
+                                }
+                            } else {
+                                if (lane == 0) mbar_arrive_expect_tx(&B.full[st], C::kSlot);
+                                __syncwarp();
+                                if (lane < TN / run) {
 #pragma unroll
-                            for (int b = 0; b < C::kBlocks; ++b)
-                                tma_load_2d(dst + b * C::kBlock, kv ? &map_v : &map_k, &B.full[st], 64 * b, row);
+                                    for (int b = 0; b < C::kBlocks; ++b)
+                                        tma_load_3d(dst + b * C::kBlock + lane * run * 128, kv ? &map_v : &map_k, &B.full[st],
+                                                    0, row, b);
+                                }
+                            }
+                            __syncwarp();
                         }
+                        if (++st == C::kSlots) st = 0, par ^= 1;
                     }
                 }
             }
@@ -291,9 +314,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         if (!ok) fail();
         // no copy may land after the CTA is gone
         if (lane == 0)
-            for (int st = 0; st < 7; ++st)
-                if ((last_full >> st) & 1)
-                    mbar_wait(E4M3 ? &B.rfull[st < 3 ? st : 0] : &B.full[st], (last_par >> st) & 1, kDrainWaitNs);
+            for (int x = 0; x < (E4M3 ? C::kRawSlots : C::kSlots); ++x)
+                if ((last_full >> x) & 1) mbar_wait(E4M3 ? &B.rfull[x] : &B.full[x], (last_par >> x) & 1, kDrainWaitNs);
         __syncwarp();
     } else if (warp >= kConvWarp0) {
         // =================================================== conversion, last tiles
@@ -337,40 +359,38 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         uint8_t* out0 = slot + sw128_off(tok0, 2 * col);
                         uint8_t* out1 = slot + sw128_off(tok0, 2 * col + 1);
                         const bool whole = left >= TN;
+                        constexpr int kAhead = C::kBlocks > 1 ? 4 : 2;  // pieces: two tokens of one or two blocks
 #pragma unroll
-                        for (int y = 0; y < C::kBlocks; ++y) {
-                            const int block = C::kBlocks > 1 ? y ^ h : 0;
+                        for (int y0 = 0; y0 < C::kBlocks; y0 += kAhead / 2) {
+                            uint4 u[kAhead];
 #pragma unroll
-                            for (int j0 = 0; j0 < TN; j0 += 64) {
-                                uint4 u[2];
+                            for (int j = 0; j < kAhead; ++j) {
+                                const int block = C::kBlocks > 1 ? (y0 + j / 2) ^ h : 0;
+                                u[j] = *reinterpret_cast<const uint4*>(in + 32 * (j & 1) * D + 64 * block);
+                                if (!whole && tok0 + 32 * (j & 1) >= left) u[j] = make_uint4(0, 0, 0, 0);
+                            }
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    u[j] = *reinterpret_cast<const uint4*>(in + (j0 + 32 * j) * D + 64 * block);
-                                    if (!whole && tok0 + j0 + 32 * j >= left) u[j] = make_uint4(0, 0, 0, 0);
-                                }
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int at = block * C::kBlock + (j0 + 32 * j) * 128;
-                                    *reinterpret_cast<uint4*>(out0 + at) =
-                                        make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
-                                                   e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
-                                    *reinterpret_cast<uint4*>(out1 + at) =
-                                        make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
-                                                   e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
-                                }
+                            for (int j = 0; j < kAhead; ++j) {
+                                const int at = (C::kBlocks > 1 ? (y0 + j / 2) ^ h : 0) * C::kBlock + 32 * (j & 1) * 128;
+                                *reinterpret_cast<uint4*>(out0 + at) =
+                                    make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
+                                               e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
+                                *reinterpret_cast<uint4*>(out1 + at) =
+                                    make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
+                                               e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
                             }
                         }
                         publish(&B.full[st]);
                         if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
                     } else {
-                        if (!by_hand(seg, tile)) continue;
+                        if (kv != warp - kConvWarp0 || !by_hand(seg, tile)) continue;  // a warp for keys, one for values
                         if (!all_wait(&B.hand[st], (hand_par >> st) & 1, abort_flag, wlim)) { ok = false; break; }
                         hand_par ^= 1u << st;
                         constexpr int kPer = D / 8;
                         const int draft = seg.seq.len - seg.seq.nodes - tile * TN;  // the draft's first token here
                         bool odd = false;
-#pragma unroll 2
-                        for (int y = pt; y < TN * kPer; y += kConvThreads) {
+#pragma unroll 4
+                        for (int y = lane; y < TN * kPer; y += 32) {
                             const int tok = y / kPer, col = y % kPer;
                             uint4 u = make_uint4(0, 0, 0, 0);
                             if (tok < left) {
@@ -403,60 +423,56 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         // is a constant added to the address field.
         const uint64_t kd = sw128_desc(smem_u32(sm), 16, 1024), vd = sw128_desc(smem_u32(sm), C::kBlock, 1024);
         int ks = 0, vs = 1, kpar = 0, vpar = 0;  // slots of the next keys and values, their phases
-        auto advance = [](int& st, int& par) {   // two groups further
-            st += 2;
-            if (st >= C::kSlots) {
-                st -= C::kSlots;
-                par ^= 1;
-            }
-        };
-        auto scores = [&](int b) -> bool {  // S of the next tile into buffer b
+        int sb = 0, pb = 0, ppar = 0;            // buffers of the next scores and probabilities
+        auto scores = [&]() -> bool {            // S of the next tile
             if (!all_wait(&B.full[ks], kpar, abort_flag, wlim)) return false;
             tc_fence_after();
             const uint64_t d0 = kd + (uint64_t)(ks * (C::kSlot >> 4));
-            const uint32_t s0 = tmem + C::kColS + b * TN;
+            const uint32_t s0 = tmem + C::kColS + sb * TN;
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_bf16_ta(s0, tmem + C::kColQ + 8 * kk, d0 + (((kk >> 2) * C::kBlock + 32 * (kk & 3)) >> 4), C::kIdescS,
                                 kk > 0);
-                mma_commit(&B.sfull[b]);
+                mma_commit(&B.sfull[sb]);
                 mma_commit(&B.empty[ks]);
             }
             __syncwarp();
-            advance(ks, kpar);
+            if ((ks += 2) >= C::kSlots) ks = 0, kpar ^= 1;
+            if (++sb == C::kBufs) sb = 0;
             return true;
         };
-        int b = 0, ppar = 0;
-        if (have) ok = all_wait(&B.qfull, 0, abort_flag, wlim) && scores(0);
+        int og = 0;  // accumulator of the next tile
         for (int seg_no = 0; ok && have; ++seg_no) {
             const int tiles = seg.tile1 - seg.tile0;
-            const bool more = next_segment<kTcRows, TN>(a, share, seg);
-            if (seg_no > 0) ok = all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim);
+            ok = all_wait(&B.qfull, seg_no & 1, abort_flag, wlim);
+            for (int y = 0; ok && y < tiles && y < C::kBufs; ++y) ok = scores();
+            if (ok && seg_no > 0) ok = all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim);
             for (int y = 0; ok && y < tiles; ++y) {
-                // the next scores first: of this segment, or (below) of the next one
-                if (y + 1 < tiles && !scores(b ^ 1)) { ok = false; break; }
-                if (!all_wait(&B.full[vs], vpar, abort_flag, wlim) || !all_wait(&B.pfull[b], ppar, abort_flag, wlim)) {
+                if (!all_wait(&B.full[vs], vpar, abort_flag, wlim) || !all_wait(&B.pfull[pb], ppar, abort_flag, wlim)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint64_t d0 = vd + (uint64_t)(vs * (C::kSlot >> 4));
-                const uint32_t p0 = tmem + C::kColS + b * TN;
+                const uint32_t p0 = tmem + C::kColS + pb * TN;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < TN / 16; ++kk)
-                        mma_bf16_ta(tmem, p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO, y > 0 || kk > 0);
-                    mma_commit(&B.odone);
+                        mma_bf16_ta(tmem + (C::kGroups ? og * D : 0), p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO,
+                                    y >= (C::kGroups ? 2 : 1) || kk > 0);
                     mma_commit(&B.empty[vs]);
+                    mma_commit(&B.odone[C::kGroups ? og : 0]);
+                    if (y + 1 == tiles) mma_commit(&B.oend);
                 }
                 __syncwarp();
-                advance(vs, vpar);
-                b ^= 1;
-                if (b == 0) ppar ^= 1;
+                if ((vs += 2) >= C::kSlots) vs = 1, vpar ^= 1;
+                if (++pb == C::kBufs) pb = 0, ppar ^= 1;
+                og ^= 1;
+                // the buffer of these probabilities takes the scores kBufs tiles on
+                if (y + C::kBufs < tiles) ok = scores();
             }
-            if (ok && more) ok = all_wait(&B.qfull, (seg_no + 1) & 1, abort_flag, wlim) && scores(b);
-            have = more;
+            have = ok && next_segment<kTcRows, TN>(a, share, seg);
         }
         if (!ok && lane == 0) fail();
         if (elect_one()) mma_commit(&B.drain);
@@ -464,13 +480,12 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         mbar_wait(&B.drain, 0, kDrainWaitNs);
     } else {
         // ================================================================= softmax
-        constexpr int HC = TN / 2;  // tokens of this warp's half
-        const int quarter = warp & 3, half = warp >> 2;
-        const int m = 32 * quarter + lane;  // row of the tile, lane of tensor memory
-        const int pair = 1 + quarter;       // named barrier of the two warps
+        const int quarter = warp & 3, half = warp >> 2;  // half: of the columns, or the group
+        const int m = 32 * quarter + lane;               // row of the tile, lane of tensor memory
+        const int pair = 1 + quarter;                    // named barrier of the two warps with the same rows
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-        int i = 0;
-        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
+        int i = 0;  // tile number in this CTA
+        for (int seg_no = 0; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg), ++seg_no) {
             const bool busy = 32 * quarter < seg.rows, live = m < seg.rows;
             const int r = seg.rt * kTcRows + (live ? m : 0);
             const int node = r / G, head = seg.hk * G + r % G;
@@ -483,8 +498,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             }
             float ref = kNegInf, mul = a.scale * kLog2e;
             float2 l2 = make_float2(0.f, 0.f);
-            // ---- queries to tensor memory: half of the row per warp (the products that read
-            // the last segment's are done: their scores have been here)
+            // ---- queries, half of the row per warp (every product that reads the last
+            // segment's is done)
             if (busy) {
                 const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
                                                                  (int64_t)head * D + half * (D / 2));
@@ -528,132 +543,242 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.qfull);
             if (E4M3 && busy) pair_sync(pair);  // (what the warps told each other is read)
-            for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++i) {
-                const int b = i & 1;
-                // A warp whose wait runs out goes on to the vote below, where its partner
-                // learns of it: neither may stay alone at their barrier.
-                ok = all_wait(&B.sfull[b], (i >> 1) & 1, abort_flag, wlim) &&
-                     (!E4M3 || all_wait(&B.cfull[i % kScaleSlots], (i / kScaleSlots) & 1, abort_flag, wlim)) && ok;
-                tc_fence_after();
-                if (busy) {
-                    const uint32_t s0 = tmem + lane_off + C::kColS + b * TN;
-                    const float* sc = scales + (i % kScaleSlots) * 3 * TN + half * HC;
-                    const int off = tile * TN + half * HC - base;  // this half's start past the context
-                    const bool masked = off + HC > 0;
-                    float2 s[HC / 2];
+
+            const int tiles = seg.tile1 - seg.tile0, i1 = i + tiles;
+            if constexpr (C::kGroups) {
+                // ---- this group's tiles: scores in two passes of 32 columns at a time
+                const int first = i + ((i ^ half) & 1);
+                for (int x = first; x < i1; x += 2) {
+                    const int tile = seg.tile0 + x - i;
+                    ok = all_wait(&B.sfull[x % 3], (x / 3) & 1, abort_flag, wlim) &&
+                         (!E4M3 || all_wait(&B.cfull[x % kScaleSlots], (x / kScaleSlots) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (busy) {
+                        const uint32_t s0 = tmem + lane_off + C::kColS + (x % 3) * TN;
+                        const float* sc = scales + (x % kScaleSlots) * 3 * TN;
+                        const int off = tile * TN - base;  // the tile's start past the context
+                        auto softmax = [&](auto masked_) {
+                            constexpr bool masked = decltype(masked_)::value;
+                            const float2 mul_2 = make_float2(mul, mul);
+                            float top = kNegInf, top_b = kNegInf;
 #pragma unroll
-                    for (int c0 = 0; c0 < HC; c0 += 32)
-                        tmem_ld32(s0 + half * HC + c0, *reinterpret_cast<float(*)[32]>(&s[c0 / 2]));
-                    tmem_wait_ld();
-                    const float2 mul_2 = make_float2(mul, mul);
-                    if (E4M3) {
-#pragma unroll
-                        for (int e = 0; e < HC / 2; e += 2) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * e);
-                            s[e] = mul2(s[e], mul2(mul_2, make_float2(k4.x, k4.y)));
-                            s[e + 1] = mul2(s[e + 1], mul2(mul_2, make_float2(k4.z, k4.w)));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < HC / 2; ++e) s[e] = mul2(s[e], mul_2);
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int c0 = 0; c0 < HC; c0 += 32) {
-                            const uint32_t bits = sees32(sees, off + c0);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                if (!((bits >> (2 * e)) & 1)) s[c0 / 2 + e].x = kNegInf;
-                                if (!((bits >> (2 * e + 1)) & 1)) s[c0 / 2 + e].y = kNegInf;
-                            }
-                        }
-                    }
-                    float top = kNegInf, top_b = kNegInf;
-#pragma unroll
-                    for (int e = 0; e < HC / 2; e += 2) {
-                        float2 y = s[e], z = s[e + 1];
-                        if (E4M3) {
-                            const float4 v4 = *reinterpret_cast<const float4*>(sc + 2 * TN + 2 * e);
-                            y = add2(y, make_float2(v4.x, v4.y));
-                            z = add2(z, make_float2(v4.z, v4.w));
-                        }
-                        top = max3(top, y.x, y.y);
-                        top_b = max3(top_b, z.x, z.y);
-                    }
-                    top = fmaxf(top, top_b);
-                    // ---- the reference: moved when either half outgrows it (both warps have
-                    // read their scores when the vote is out: probabilities may overwrite them)
-                    if (pair_any(pair, !ok || (live && top > ref + kLazy))) {
-                        row_top[half * 128 + m] = top;
-                        if (!ok) B.gave_up[warp] = 1;
-                        pair_sync(pair);
-                        ok = ok && !B.gave_up[warp ^ 4];
-                        if (!ok) break;
-                        top = fmaxf(top, row_top[(half ^ 1) * 128 + m]);
-                        const bool move = top > ref;
-                        const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
-                        if (move) ref = top;
-                        l2 = mul2(l2, make_float2(f, f));
-                        if (tile != seg.tile0) {
-                            if (!all_wait(&B.odone, (i - 1) & 1, abort_flag, wlim)) ok = false;
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
-                                float o[32];
-                                tmem_ld32(tmem + lane_off + c0, o);
+                            for (int c0 = 0; c0 < TN; c0 += 32) {
+                                float2 s[16];
+                                tmem_ld32(s0 + c0, *reinterpret_cast<float(*)[32]>(&s[0]));
                                 tmem_wait_ld();
+                                if (E4M3) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= f;
-                                tmem_st32(tmem + lane_off + c0, o);
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const float4 k4 = *reinterpret_cast<const float4*>(sc + c0 + 2 * e);
+                                        const float4 v4 = *reinterpret_cast<const float4*>(sc + 2 * TN + c0 + 2 * e);
+                                        s[e] = fma2(s[e], mul2(mul_2, make_float2(k4.x, k4.y)), make_float2(v4.x, v4.y));
+                                        s[e + 1] = fma2(s[e + 1], mul2(mul_2, make_float2(k4.z, k4.w)), make_float2(v4.z, v4.w));
+                                    }
+                                }
+                                if (masked) {
+                                    const uint32_t bits = sees32(sees, off + c0);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        if (!((bits >> (2 * e)) & 1)) s[e].x = kNegInf;
+                                        if (!((bits >> (2 * e + 1)) & 1)) s[e].y = kNegInf;
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) {
+                                    top = max3(top, s[e].x, s[e].y);
+                                    top_b = max3(top_b, s[e + 1].x, s[e + 1].y);
+                                }
+                            }
+                            top = fmaxf(top, top_b);
+                            if (!E4M3) top *= mul;  // (the scale is positive)
+                            // ---- the reference: moved when outgrown
+                            const bool move = top > ref + kLazy;
+                            if (__any_sync(0xffffffffu, move)) {
+                                const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
+                                if (move) ref = top;
+                                if (x != first && __any_sync(0xffffffffu, f != 1.f)) {
+                                    l2 = mul2(l2, make_float2(f, f));
+                                    // the group's last output product (the scores of its tile before
+                                    // are complete, and with them the one before that)
+                                    if (!all_wait(&B.odone[half], ((x >> 1) - 1) & 1, abort_flag, wlim)) ok = false;
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int c0 = 0; c0 < D; c0 += 32) {
+                                        float o[32];
+                                        tmem_ld32(tmem + lane_off + half * D + c0, o);
+                                        tmem_wait_ld();
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                                        tmem_st32(tmem + lane_off + half * D + c0, o);
+                                    }
+                                    tmem_wait_st();
+                                }
+                            }
+                            const float minus = ref == kNegInf ? 0.f : -ref;
+                            const float2 minus_2 = make_float2(minus, minus);
+#pragma unroll
+                            for (int c0 = 0; c0 < TN; c0 += 32) {
+                                float2 s[16];
+                                tmem_ld32(s0 + c0, *reinterpret_cast<float(*)[32]>(&s[0]));
+                                tmem_wait_ld();
+                                const uint32_t bits = masked ? sees32(sees, off + c0) : 0xFFFFFFFFu;
+                                uint32_t p[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    float2 k2 = mul_2;
+                                    if (E4M3) k2 = mul2(mul_2, *reinterpret_cast<const float2*>(sc + c0 + 2 * e));
+                                    float2 y = fma2(s[e], k2, minus_2);
+                                    y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                    if (masked) {  // nothing from a token that the row does not see
+                                        if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
+                                        if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
+                                    }
+                                    l2 = add2(l2, y);
+                                    if (E4M3) {
+                                        y = mul2(y, *reinterpret_cast<const float2*>(sc + TN + c0 + 2 * e));
+                                        if (masked) {  // (whatever its scale)
+                                            if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
+                                            if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
+                                        }
+                                    }
+                                    p[e] = E4M3 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                                }
+                                tmem_st16(s0 + c0 / 2, p);
                             }
                             tmem_wait_st();
-                        }
-                        pair_sync(pair);  // the maxima are read
+                        };
+                        if (off + TN > 0) softmax(Bool<true>{});
+                        else softmax(Bool<false>{});
                     }
-                    const float minus = ref == kNegInf ? 0.f : -ref;
-                    const float2 minus_2 = make_float2(minus, minus);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B.pfull[x % 3]);
+                    if (!ok) break;
+                }
+            } else {
+                // ---- half of every tile's columns
+                constexpr int HC = TN / 2;
+                for (int x = i; x < i1; ++x) {
+                    const int tile = seg.tile0 + x - i, b = x & 1;
+                    // A warp whose wait runs out goes on to the vote below, where its partner
+                    // learns of it: neither may stay alone at their barrier.
+                    ok = all_wait(&B.sfull[b], (x >> 1) & 1, abort_flag, wlim) &&
+                         (!E4M3 || all_wait(&B.cfull[x % kScaleSlots], (x / kScaleSlots) & 1, abort_flag, wlim)) && ok;
+                    tc_fence_after();
+                    if (busy) {
+                        const uint32_t s0 = tmem + lane_off + C::kColS + b * TN;
+                        const float* sc = scales + (x % kScaleSlots) * 3 * TN + half * HC;
+                        const int off = tile * TN + half * HC - base;  // this half's start past the context
+                        const bool masked = off + HC > 0;
+                        const uint32_t bits = masked ? sees32(sees, off) : 0xFFFFFFFFu;
+                        static_assert(HC == 32 || C::kGroups, "one load per half");
+                        float2 s[16];
+                        tmem_ld32(s0 + half * HC, *reinterpret_cast<float(*)[32]>(&s[0]));
+                        tmem_wait_ld();
+                        const float2 mul_2 = make_float2(mul, mul);
 #pragma unroll
-                    for (int c0 = 0; c0 < HC; c0 += 32) {
-                        const uint32_t bits = E4M3 && masked ? sees32(sees, off + c0) : 0xFFFFFFFFu;
-                        uint32_t p[16];
+                        for (int e = 0; e < 16; ++e) {
+                            float2 k2 = mul_2;
+                            if (E4M3) k2 = mul2(mul_2, *reinterpret_cast<const float2*>(sc + 2 * e));
+                            s[e] = mul2(s[e], k2);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                if (!((bits >> (2 * e)) & 1)) s[e].x = kNegInf;
+                                if (!((bits >> (2 * e + 1)) & 1)) s[e].y = kNegInf;
+                            }
+                        }
+                        float top = kNegInf, top_b = kNegInf;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
-                            float2 y = add2(s[c0 / 2 + e], minus_2), z = add2(s[c0 / 2 + e + 1], minus_2);
-                            y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            z = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-                            l2 = add2(l2, add2(y, z));
+                            float2 y = s[e], z = s[e + 1];
                             if (E4M3) {
-                                const float4 v4 = *reinterpret_cast<const float4*>(sc + TN + c0 + 2 * e);
-                                y = mul2(y, make_float2(v4.x, v4.y));
-                                z = mul2(z, make_float2(v4.z, v4.w));
+                                const float4 v4 = *reinterpret_cast<const float4*>(sc + 2 * TN + 2 * e);
+                                y = add2(y, make_float2(v4.x, v4.y));
+                                z = add2(z, make_float2(v4.z, v4.w));
+                            }
+                            top = max3(top, y.x, y.y);
+                            top_b = max3(top_b, z.x, z.y);
+                        }
+                        top = fmaxf(top, top_b);
+                        // ---- the reference: moved when either half outgrows it (both warps have
+                        // read their scores when the vote is out: probabilities may overwrite them)
+                        if (pair_any(pair, !ok || (live && top > ref + kLazy))) {
+                            row_top[half * 128 + m] = top;
+                            if (!ok) B.gave_up[warp] = 1;
+                            pair_sync(pair);
+                            ok = ok && !B.gave_up[warp ^ 4];
+                            if (!ok) break;
+                            top = fmaxf(top, row_top[(half ^ 1) * 128 + m]);
+                            const bool move = top > ref;
+                            const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
+                            if (move) ref = top;
+                            l2 = mul2(l2, make_float2(f, f));
+                            if (x != i) {
+                                if (!all_wait(&B.odone[0], (x - 1) & 1, abort_flag, wlim)) ok = false;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+                                    float o[32];
+                                    tmem_ld32(tmem + lane_off + c0, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                                    tmem_st32(tmem + lane_off + c0, o);
+                                }
+                                tmem_wait_st();
+                            }
+                            pair_sync(pair);  // the maxima are read
+                        }
+                        const float minus = ref == kNegInf ? 0.f : -ref;
+                        const float2 minus_2 = make_float2(minus, minus);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float2 y = add2(s[e], minus_2);
+                            y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            l2 = add2(l2, y);
+                            if (E4M3) {
+                                y = mul2(y, *reinterpret_cast<const float2*>(sc + TN + 2 * e));
                                 if (masked) {  // nothing from a token that the row does not see, whatever its scale
                                     if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
                                     if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
-                                    if (!((bits >> (2 * e + 2)) & 1)) z.x = 0.f;
-                                    if (!((bits >> (2 * e + 3)) & 1)) z.y = 0.f;
                                 }
                             }
                             p[e] = E4M3 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-                            p[e + 1] = E4M3 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
                         }
-                        tmem_st16(s0 + (half * HC + c0) / 2, p);
+                        tmem_st16(s0 + half * HC / 2, p);
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B.pfull[b]);
+                    if (!busy && !ok) break;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B.pfull[b]);
-                if (!busy && !ok) break;
             }
             // ---- the segment's output
-            ok = ok && all_wait(&B.odone, (i - 1) & 1, abort_flag, wlim);
+            const int i0 = i;
+            i = i1;
+            ok = ok && all_wait(&B.oend, seg_no & 1, abort_flag, wlim);
             if (busy ? pair_any(pair, !ok) : !ok) { ok = false; break; }
             tc_fence_after();
             const bool odd = !E4M3 && *reinterpret_cast<volatile int*>(&B.odd) != 0;
             if (busy) {
-                row_top[half * 128 + m] = l2.x + l2.y;
+                row_top[half * 128 + m] = ref;
+                row_sum[half * 128 + m] = l2.x + l2.y;
                 pair_sync(pair);
-                const float l = row_top[m] + row_top[128 + m];
+                // the two sums under one reference; a group without a tile has no output
+                const float ref_0 = row_top[m], ref_1 = row_top[128 + m];
+                float l = 0.f, f_0 = 1.f, f_1 = 1.f;
+                if (C::kGroups) {
+                    ref = fmaxf(ref_0, ref_1);
+                    f_0 = ref_0 == kNegInf ? 1.f : exp2_approx(ref_0 - ref);  // (nothing but zeros, or NaN)
+                    f_1 = ref_1 == kNegInf ? 1.f : exp2_approx(ref_1 - ref);
+                }
+                l = row_sum[m] * f_0 + row_sum[128 + m] * f_1;
+                const bool have_0 = !C::kGroups || tiles > 1 || !(i0 & 1), have_1 = C::kGroups && (tiles > 1 || (i0 & 1));
                 const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
                 const bool empty = ref == kNegInf && l == 0.f;
                 const float inv = empty ? 0.f : 1.f / l;
@@ -667,8 +792,21 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
 #pragma unroll 1
                 for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                     float o[32];
-                    tmem_ld32(tmem + lane_off + c0, o);
-                    tmem_wait_ld();
+                    if (have_0) {
+                        tmem_ld32(tmem + lane_off + c0, o);
+                        tmem_wait_ld();
+                    }
+                    if (C::kGroups) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = have_0 ? o[e] * f_0 : 0.f;
+                        if (have_1) {
+                            float o1[32];
+                            tmem_ld32(tmem + lane_off + D + c0, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f_1, o[e]);
+                        }
+                    }
                     if (!live) continue;
                     if (odd) {
                         // drafted values that are not finite, for the rows that see them
@@ -711,7 +849,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 }
                 if (whole && live && half == 0 && a.lse)
                     a.lse[t * a.H + head] = empty ? kNegInf : ref * kLn2 + logf(l);
-                pair_sync(pair);  // the sums are read
+                pair_sync(pair);  // what the warps told each other is read
             }
             tc_fence_before();
             __syncwarp();
@@ -741,16 +879,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// The cache's rows [n_pages * Hk * page, D] bf16; boxes of 64 elements x the
-// rows of a page that one tile can take, 128-byte swizzle.
+// The cache's rows [n_pages * Hk * page, D] bf16 as (64 elements, row, block of 64
+// elements); boxes of the rows of a page that one tile can take, 128-byte
+// swizzle: all blocks at once where that is the whole tile, else one.
 bool make_map(CUtensorMap* m, const void* ptr, const CacheView& c, int rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)((c.n_pages * c.Hk) << c.page_shift)};
-    cuuint64_t strides[1] = {(cuuint64_t)c.D * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+    cuuint64_t dims[3] = {64, (cuuint64_t)((c.n_pages * c.Hk) << c.page_shift), (cuuint64_t)(c.D / 64)};
+    cuuint64_t strides[2] = {(cuuint64_t)c.D * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)rows, rows == TN ? (cuuint32_t)(c.D / 64) : 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -759,11 +898,11 @@ template <int D, bool E4M3>
 cudaError_t launch_tc(const TreeArgs& a, cudaStream_t s) {
     using C = Tc<D, E4M3>;
     CUtensorMap mk = {}, mv = {};
-    const int page = 1 << a.c.page_shift, run = page < C::TN ? page : C::TN;
+    const int page = 1 << a.c.page_shift, run = page < TN ? page : TN;
     if (!E4M3 && (!make_map(&mk, a.c.k, a.c, run) || !make_map(&mv, a.c.v, a.c, run))) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    tree_tc_kernel<D, E4M3><<<a.grid, kTcThreads, C::kSmem, s>>>(a, mk, mv);
+    tree_tc_kernel<D, E4M3><<<a.grid, C::kThreads, C::kSmem, s>>>(a, mk, mv);
     return cudaGetLastError();
 }
 
