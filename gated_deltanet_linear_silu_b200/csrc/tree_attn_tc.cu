@@ -225,7 +225,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         }
     };
     const int page = 1 << a.c.page_shift;
-    const int run = page < TN ? page : TN;  // tokens of one page in a tile
+    const int run_shift = a.c.page_shift < 6 ? a.c.page_shift : 6;  // tokens of one page in a tile
+    const int run = 1 << run_shift, runs = TN >> run_shift;
+    static_assert(TN == 64, "run_shift");
     // bf16 tiles that the converters fill: with drafted tokens, or past the sequence's end
     auto by_hand = [&](const Segment& g, int tile) {
         return !E4M3 && (tile + 1) * TN > g.seq.len - g.seq.nodes;
@@ -248,15 +250,14 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             // table is read one tile ahead, and what is read is not looked at before
             // its tile comes.
             const int at = run == TN ? 0 : lane;
+            const int32_t* table = a.p.table + (int64_t)seg.n * a.p.max_pages;
             auto page_id = [&](int tile) -> int {
                 const int pos = tile * TN + at * run;
-                return tile < seg.tile1 && at < TN / run && pos < seg.seq.len
-                           ? __ldg(a.p.table + (int64_t)seg.n * a.p.max_pages + (pos >> a.c.page_shift))
-                           : 0;
+                return tile < seg.tile1 && at < runs && pos < seg.seq.len ? __ldg(table + (pos >> a.c.page_shift)) : 0;
             };
             int next_id = page_id(seg.tile0);
             for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
-                const int n_runs = min(TN / run, (min(TN, seg.seq.len - tile * TN) + run - 1) / run);
+                const int n_runs = (min(TN, seg.seq.len - tile * TN) + run - 1) >> run_shift;
                 int id = next_id;
                 next_id = page_id(tile + 1);
                 if (id < 0 || id >= a.c.n_pages) {
@@ -297,7 +298,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             } else {
                                 if (lane == 0) mbar_arrive_expect_tx(&B.full[st], C::kSlot);
                                 __syncwarp();
-                                if (lane < TN / run) {
+                                if (lane < runs) {
 #pragma unroll
                                     for (int b = 0; b < C::kBlocks; ++b)
                                         tma_load_3d(dst + b * C::kBlock + lane * run * 128, kv ? &map_v : &map_k, &B.full[st],
