@@ -1,9 +1,10 @@
-"""Build libgdn.so in-tree for sm_100a with nvcc (no GPU needed).
+"""Build libgdn.so (nvcc, sm_100a) and _binding.so (the host compiler, against
+PyTorch's headers) in-tree; no GPU needed.
 
     python -m gated_deltanet_linear_silu_b200.build [--force]
 
-Objects go to _build/ at the repository root; the shared library is written
-next to this file, where the Python binding loads it.
+Objects go to _build/ at the repository root; the shared libraries are written
+next to this file, where the Python binding loads them.
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -42,11 +45,41 @@ def _deps():
         [os.path.join(INCLUDE, "gdn.h"), os.path.abspath(__file__)]
 
 
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "gdn.h"), os.path.abspath(__file__)])
+
+
+def build_binding() -> str:
+    """The Python entry points in C++ (csrc/binding.cpp). They link PyTorch's
+    libraries by name: the interpreter has them loaded when it imports this."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler: g++ is required to build the Python binding")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for i in inc for x in ("-isystem", i)], BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -64,10 +97,15 @@ def _compile(src: str, verbose: bool) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        if not binding_up_to_date():
+            build_binding()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = None if not force and binding_up_to_date() else ex.submit(build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), _sources()))
+        if binding is not None:
+            binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "--no-undefined"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -586,6 +586,63 @@ def test_cache_past_32_bits():
     gdn.check_device_status(DEV)
 
 
+# ---------------------------------------------------------------- tensors that are refused
+
+def test_refused_tensors():
+    """Shapes, types, strides and devices that the C ABI cannot see."""
+    z = lambda *s, d=BF, dev=DEV: torch.zeros(s, dtype=d, device=dev)
+    i32, f64 = torch.int32, torch.float64
+    q, k, w, pos, f = z(3, 4, 64), z(3, 2, 64), z(64, d=F32), z(3, d=i32), z(16, d=f64)
+    ok = [q, k, w, w, pos, f]
+    gdn.qk_norm_rope(*ok)
+    bad = [(1, z(2, 2, 64)), (1, z(3, 2, 32)), (1, k.float()), (2, w.double()), (2, z(32, d=F32)), (4, pos.long()),
+           (4, z(4, d=i32)), (5, f.float()), (5, z(33, d=f64)), (0, q[0]), (2, w.cpu()), (4, z(6, d=i32)[::2]),
+           (0, z(3, 4, 128)[..., ::2]), (0, z(3, 64, 4).transpose(1, 2))]
+    for i, x in bad:
+        args = list(ok)
+        args[i] = x
+        with pytest.raises((ValueError, TypeError)):
+            gdn.qk_norm_rope(*args)
+    with pytest.raises(TypeError):
+        gdn.qk_norm_rope(q.half(), k.half(), w, w, pos, f)
+    with pytest.raises(ValueError):
+        gdn.qk_norm_rope(*ok, out_q=z(3, 4, 64, d=F32))
+    pool = Pool([20], [3], 2, 64, 16, F8)
+    c, pages = pool.cache, pool.where
+    gdn.kv_cache_write(k, k, c, *pages)
+    for held in (c._replace(v=z(*c.k.shape)), c._replace(k_scale=None), c._replace(v_scale=c.v_scale.double()),
+                 c._replace(k_scale=c.k_scale[..., :8]), c._replace(k=c.k.cpu(), v=c.v.cpu()),
+                 gdn.KVCache(z(2, 2, 16, 64, d=F32), z(2, 2, 16, 64, d=F32)), c._replace(k=c.k[0], v=c.v[0])):
+        with pytest.raises((ValueError, TypeError)):
+            gdn.kv_cache_write(k, k, held, *pages)
+    for p in ((pages[0].long(), *pages[1:]), (pages[0][0], *pages[1:]), (pages[0], pages[1].repeat(2), pages[2]),
+              (pages[0], pages[1], pages[2][:0]), (pages[0].cpu(), *pages[1:]), (pages[0].repeat(2, 1), *pages[1:])):
+        with pytest.raises((ValueError, TypeError)):
+            gdn.kv_cache_write(k, k, c, *p)
+    for a, b in ((k, z(3, 1, 64)), (z(3, 1, 64), z(3, 1, 64)), (k, k.float()), (k[0], k[0])):
+        with pytest.raises(ValueError):
+            gdn.kv_cache_write(a, b, c, *pages)
+    with pytest.raises(ValueError):
+        gdn.kv_cache_read(c, *pages, n_tokens=-1)
+    with pytest.raises(ValueError):
+        gdn.kv_cache_read(c, *pages, n_tokens=3, out_k=z(4, 2, 64))
+    with pytest.raises(ValueError):
+        gdn.kv_cache_accept(c, *pages, z(2, 4, d=i32))
+    with pytest.raises(gdn.GDNError):
+        gdn.kv_cache_accept(c, *pages, z(1, 4, d=i32), out_seq_lens=pages[1])
+    with pytest.raises(ValueError):
+        gdn.tree_attention(z(3, 4, 128), c, *pages, max_nodes=3)
+    with pytest.raises(gdn.GDNError):
+        gdn.tree_attention(z(3, 3, 64), c, *pages, max_nodes=3)
+    with pytest.raises(gdn.GDNError):
+        gdn.tree_attention(q.float(), c, *pages, max_nodes=3)
+    for kw in (dict(mask=z(2, d=torch.int64)), dict(mask=pos), dict(gate=z(3, 4, 64, d=F32)), dict(out=z(3, 2, 64)),
+               dict(workspace=z(64, d=torch.uint8)[::2])):
+        with pytest.raises(ValueError):
+            gdn.tree_attention(q, c, *pages, max_nodes=3, **kw)
+    gdn.check_device_status(DEV)
+
+
 # ---------------------------------------------------------------- as a serving loop runs them
 
 def test_streams_graphs_and_workspaces():

@@ -8,7 +8,7 @@ import torch
 
 import gated_deltanet_linear_silu_b200 as gdn
 from gated_deltanet_linear_silu_b200 import build as gbuild
-from gated_deltanet_linear_silu_b200.softmax_attention import _CacheStruct, _cache_arg, _pages
+from gated_deltanet_linear_silu_b200.softmax_attention import _CacheStruct
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 A = 1 << 20  # aligned, never dereferenced: validation fails first
@@ -162,32 +162,33 @@ def test_workspace_size(L):
     assert size(None, 4, 8, 8) == size(cache(D=96), 4, 8, 8) == size(cache(), 4, 8, 0) == size(cache(), -1, 8, 8) == 0
 
 
-def test_binding_refuses_tensors():
+def test_binding_refuses_tensors(L):
+    """What can be seen without a device: shapes, types and host tensors."""
     t = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d)
-    f8, f32, i32, i64 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
-    with pytest.raises(ValueError):  # host tensors
-        _cache_arg(gdn.KVCache(t(2, 1, 16, 64), t(2, 1, 16, 64)))
-    with pytest.raises(ValueError):  # k and v alike
-        _cache_arg(gdn.KVCache(t(2, 1, 16, 64), t(2, 1, 16, 128)))
-    with pytest.raises(ValueError):  # an e4m3 cache has scales
-        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f8), t(2, 1, 16, 64, d=f8)))
-    with pytest.raises(TypeError):
-        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f8), t(2, 1, 16, 64, d=f8), t(2, 1, 16), t(2, 1, 16)))
-    with pytest.raises(TypeError):
-        _cache_arg(gdn.KVCache(t(2, 1, 16, 64, d=f32), t(2, 1, 16, 64, d=f32)))
+    f8, f32, i32, f64 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.float64
     with pytest.raises(TypeError):
         gdn.kv_cache(2, 16, 1, 64, dtype=f32, device="cpu")
-    with pytest.raises(TypeError):
-        _pages(t(1, 2, d=i64), t(1, d=i32), t(2, d=i32))
-    with pytest.raises(ValueError):
-        _pages(t(2, 2, d=i32), t(1, d=i32), t(2, d=i32))
     q, k, w = t(3, 4, 64), t(3, 2, 64), t(64, d=f32)
-    pos, f = t(3, d=i32), t(16, d=torch.float64)
-    for bad in [(q, t(2, 2, 64), w, w, pos, f), (q, k.float(), w, w, pos, f), (q, k, w.double(), w, pos, f),
-                (q, k, w, t(32, d=f32), pos, f), (q, k, w, w, pos.long(), f), (q, k, w, w, pos, f.float()),
-                (q, k, w, w, pos, t(33, d=torch.float64)), (q, k, w, w, pos, f)]:  # the last: host tensors
-        with pytest.raises(ValueError):
-            gdn.qk_norm_rope(*bad)
+    pos, f = t(3, d=i32), t(16, d=f64)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.qk_norm_rope(q, k, w, w, pos, f)
+    held = gdn.kv_cache(2, 16, 2, 64, device="cpu")
+    pages = (t(1, 2, d=i32), t(1, d=i32), t(2, d=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.qk_norm_rope_cache(q, k, k, w, w, pos, f, held, *pages)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.kv_cache_write(k, k, held, *pages)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.kv_cache_read(held, *pages, n_tokens=3)
+    with pytest.raises(TypeError):
+        gdn.kv_cache_read(held, *pages, n_tokens=3, dtype=torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.kv_cache_accept(held, *pages, t(1, 4, d=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.tree_attention(q, held, *pages, max_nodes=3)
+    with pytest.raises(TypeError):
+        gdn.kv_cache_write(None, k, held, *pages)
+    assert f8 == held.k.dtype
 
 
 def test_tree_mask():
