@@ -127,19 +127,23 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
 
         // ---- the ring: this warp's 16 tokens of a tile into stage st. Pages hold a
         // multiple of 16 tokens: a step lies in one, its rows back to back.
-        auto page_of = [&](int tile) -> int64_t {  // row of the step's first token; -1: nothing there
+        const int32_t* table = a.p.table + (int64_t)seg.n * a.p.max_pages;
+        auto page_id = [&](int tile) -> int {  // page of the step; looked at by issue(), a tile later
             const int pos = tile * kTile + warp * 16;
-            if (tile >= tile1 || pos >= seq.len) return -1;
-            const int64_t row = page_row(a.p, a.c, seg.n, pos);
-            if (row < 0 && lane == 0) set_status(a.status, kStatusBadSeqlens);
-            return row < 0 ? -1 : row + head_rows;
+            return tile < tile1 && pos < seq.len ? __ldg(table + (pos >> a.c.page_shift)) : 0;
         };
-        auto issue = [&](int tile, int64_t row, int st) {
+        auto issue = [&](int tile, int id, int st) {
             uint8_t* dst = ring + st * C::kStage;
-            const int left = row < 0 ? 0 : seq.len - (tile * kTile + warp * 16);  // tokens that exist
             if (tile < tile1) {
-                const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + (row < 0 ? 0 : row) * RB + 16 * lane;
-                const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + (row < 0 ? 0 : row) * RB + 16 * lane;
+                const int pos = tile * kTile + warp * 16;
+                int left = seq.len - pos;  // tokens that exist
+                if (id < 0 || id >= a.c.n_pages) {
+                    if (lane == 0) set_status(a.status, kStatusBadSeqlens);
+                    left = id = 0;
+                }
+                const int64_t row = (((int64_t)id * a.c.Hk + hk) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
+                const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + row * RB + 16 * lane;
+                const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + row * RB + 16 * lane;
                 if (left >= 16) {
 #pragma unroll
                     for (int i = 0; i < C::kSide / 512; ++i) {
@@ -156,27 +160,28 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                     for (int i = 0; i < C::kSide / 512; ++i) {
                         const int p = lane + 32 * i, tok = p / C::kChunks;
                         const bool on = tok < left;
-                        cp_async_zfill16(dst + C::offset(tok, p % C::kChunks), on ? kb + 512 * i : kb, on);
-                        cp_async_zfill16(dst + C::kSide + C::offset(tok, p % C::kChunks), on ? vb + 512 * i : vb, on);
+                        cp_async_zfill16(dst + C::offset(tok, p % C::kChunks), on ? kb + 512 * i : a.c.k, on);
+                        cp_async_zfill16(dst + C::kSide + C::offset(tok, p % C::kChunks), on ? vb + 512 * i : a.c.v, on);
                     }
                 }
                 if (E4M3) {
-                    const float* s = (lane < 16 ? a.c.k_scale : a.c.v_scale) + (row < 0 ? 0 : row);
+                    const float* s = lane < 16 ? a.c.k_scale : a.c.v_scale;
                     const bool on = (lane & 15) < left;
-                    cp_async_zfill4(dst + 2 * C::kSide + 4 * lane, s + (on ? lane & 15 : 0), on);
+                    cp_async_zfill4(dst + 2 * C::kSide + 4 * lane, on ? s + row + (lane & 15) : s, on);
                 }
             }
             cp_async_commit_group();
         };
-        int64_t next_row;
 #pragma unroll
-        for (int st = 0; st < C::kStages - 1; ++st) issue(tile0 + st, page_of(tile0 + st), st);
-        next_row = page_of(tile0 + C::kStages - 1);
+        for (int st = 0; st < C::kStages - 1; ++st) issue(tile0 + st, page_id(tile0 + st), st);
+        int next_id = page_id(tile0 + C::kStages - 1);
 
         // ---- queries: row 8 g + r as this lane's fragment column; what rows
         // 8 g + 2 c + {0, 1} (this lane's scores) see of the draft
         uint32_t qf[C::kQInSmem ? 1 : NT][C::kQInSmem ? 1 : kSteps][2];
-        float mul[NT][2], ref[NT][2], l[NT][2];
+        // factor of the scores (log2 units); reference, its negative (0 while there is
+        // none) and the weight (log2) that moves it; sum
+        float mul[NT][2], ref[NT][2], minus[NT][2], l[NT][2];
         uint64_t sees[NT][2];
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
@@ -225,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 sees[g][i] = !on ? 0 : a.mask ? (uint64_t)a.mask[seq.first + node] : (2ull << node) - 1;
                 // a row that is not there: a reference that no score reaches and beside which all vanish
                 ref[g][i] = on ? kNegInf : 1e30f;
+                minus[g][i] = on ? 0.f : -1e30f;
                 l[g][i] = 0.f;
             }
         }
@@ -245,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 int next = st + C::kStages - 1;
                 if (next >= C::kStages) next -= C::kStages;
                 __syncwarp();  // every lane has read the stage that is filled next
-                issue(tile + C::kStages - 1, next_row, next);
-                next_row = page_of(tile + C::kStages);
+                const int id = next_id;
+                next_id = page_id(tile + C::kStages);
+                issue(tile + C::kStages - 1, id, next);
             }
             cp_async_wait_group<C::kStages - 1>();
             __syncwarp();  // the other lanes' copies as well
@@ -309,65 +316,75 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                     lv[h] = log2_scale(vs[h]);
                 }
             }
-#pragma unroll
-            for (int g = 0; g < NT; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[g][e] *= E4M3 ? mul[g][e & 1] * ks[e >> 1] : mul[g][e & 1];
+            uint32_t pb[NT][2];
             const bool drafted = pos + 16 > base;  // some token is not every row's
-            uint32_t on = ~0u;                     // bit 4 g + e
-            if (drafted) {
-                on = 0;
+            auto softmax = [&](auto masked_) {
+                constexpr bool masked = decltype(masked_)::value;
+                uint32_t on = ~0u;  // bit 4 g + e
+                if (masked) {
+                    on = 0;
+#pragma unroll
+                    for (int g = 0; g < NT; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = pos + 8 * (e >> 1) + C::token(r);
+                            if (t < base || (t < seq.len && ((sees[g][e & 1] >> (t - base)) & 1))) on |= 1u << (4 * g + e);
+                        }
+                }
+                auto seen = [&](int g, int e) { return !masked || ((on >> (4 * g + e)) & 1); };
+                // s mul (+ log2 vs): largest weight of the step against the reference
+                bool grown = false;
+                float t[NT][4];
 #pragma unroll
                 for (int g = 0; g < NT; ++g)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int t = pos + 8 * (e >> 1) + C::token(r);
-                        const bool see = t < base || (t < seq.len && ((sees[g][e & 1] >> (t - base)) & 1));
-                        if (see) on |= 1u << (4 * g + e);
-                        else s[g][e] = kNegInf;
+                        if (E4M3) s[g][e] *= ks[e >> 1];
+                        t[g][e] = E4M3 ? fmaf(s[g][e], mul[g][e & 1], lv[e >> 1]) : s[g][e] * mul[g][e & 1];
+                        if (!seen(g, e)) t[g][e] = kNegInf;
+                        grown = grown || t[g][e] > ref[g][e & 1] + kLazy;
                     }
-            }
-            bool grown = false;
+                if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-            for (int g = 0; g < NT; ++g)
+                    for (int g = 0; g < NT; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) grown = grown || s[g][e] + lv[e >> 1] > ref[g][e & 1] + kLazy;
-            if (__any_sync(0xffffffffu, grown)) {
+                        for (int i = 0; i < 2; ++i) {
+                            float top = fmaxf(t[g][i], t[g][2 + i]);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            const float old = ref[g][i];
+                            if (!(top > old)) continue;
+                            ref[g][i] = top;
+                            minus[g][i] = -top;
+                            const float f = old == kNegInf ? 1.f : exp2_approx(old - top);  // nothing but zeros (or NaN) before
+                            l[g][i] *= f;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                o[j][g][i] *= f;
+                                o[j][g][2 + i] *= f;
+                            }
+                        }
+                }
 #pragma unroll
                 for (int g = 0; g < NT; ++g)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float top = fmaxf(s[g][i] + lv[0], s[g][2 + i] + lv[1]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float old = ref[g][i];
-                        if (!(top > old)) continue;
-                        ref[g][i] = top;
-                        const float f = old == kNegInf ? 1.f : exp2_approx(old - top);  // nothing but zeros (or NaN) before
-                        l[g][i] *= f;
+                    for (int h = 0; h < 2; ++h) {
+                        float w[2];
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            o[j][g][i] *= f;
-                            o[j][g][2 + i] *= f;
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = 2 * h + i;
+                            w[i] = exp2_approx(fmaf(s[g][e], mul[g][i], minus[g][i]));
+                            // a token that the row does not see adds nothing, whatever its key and scale
+                            if (!seen(g, e)) w[i] = 0.f;
+                            l[g][i] += w[i];
+                            if (E4M3) w[i] = seen(g, e) ? w[i] * vs[h] : 0.f;
                         }
+                        pb[g][h] = transpose8(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
                     }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int g = 0; g < NT; ++g)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float w[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float p = exp2_approx(s[g][2 * h + i] - (ref[g][i] == kNegInf ? 0.f : ref[g][i]));
-                        l[g][i] += p;
-                        // a token that the row does not see adds nothing, whatever its scale
-                        w[i] = !E4M3 ? p : (on >> (4 * g + 2 * h + i)) & 1 ? p * vs[h] : 0.f;
-                    }
-                    pb[g][h] = transpose8(E4M3 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
-                }
+            };
+            if (drafted) softmax(Bool<true>{});
+            else softmax(Bool<false>{});
             // ---- outputs: this lane's pieces of d x tokens labels 2c, 2c + 1 of either half
             const uint8_t* vsrc = src + C::kSide;
             constexpr int W = RB == 64 ? 2 : 4;   // words of a piece

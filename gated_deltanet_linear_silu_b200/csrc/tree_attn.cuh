@@ -20,6 +20,11 @@ namespace gdn {
 constexpr int kTcRows = 128;    // query rows of a row tile (tcgen05 kernel)
 constexpr int kTcTile = 64;     // tokens of its tiles
 constexpr int kMaxRowTiles = 32;
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // growth of a row's largest weight (log2) that moves its reference
@@ -49,12 +54,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
     return y;
 }
 
-// log2 of a value row's scale for the running reference: kept within +-100, so
-// that a weight without its scale stays in fp32's range.
+// log2 of a value row's scale for the running reference: at least -100, so that
+// a weight without its scale stays in fp32's range.
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return fminf(fmaxf(y, -100.f), 100.f);
+    return fmaxf(y, -100.f);
 }
 
 // Zeroes the halves of a bf16 pair that are not finite; true if there was one.

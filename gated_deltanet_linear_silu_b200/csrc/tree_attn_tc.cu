@@ -150,10 +150,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
     return *reinterpret_cast<float2*>(&y);
 }
-template <bool B>
-struct Bool {
-    static constexpr bool value = B;
-};
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
