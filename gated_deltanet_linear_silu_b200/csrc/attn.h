@@ -9,6 +9,9 @@
 
 namespace gdn {
 
+// Multiprocessors of the current device (148 where there is none).
+int sm_count();
+
 // Address of the device status word on the current device (api.cu).
 int* device_status_ptr();
 
@@ -97,7 +100,7 @@ struct TreeArgs {
     int* status;
     uint64_t wait_ns;  // bound on each wait of the tcgen05 kernel
     // the launch's plan (launch_tree_attention)
-    int grid, row_tiles, slot_rows, min_tiles;
+    int grid, row_tiles, slot_rows;
 };
 size_t tree_workspace_bytes(int N, int H, int Hk, int D, int max_nodes, int e4m3);
 // The tcgen05 kernel alone, for a planned launch.

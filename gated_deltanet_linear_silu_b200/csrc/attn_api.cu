@@ -1,8 +1,28 @@
 // C ABI of the softmax-attention layer's calls (declared in include/gdn.h):
 // argument validation on the host and dispatch. No allocation, no host sync.
+#include <atomic>
+
 #include "../../include/gdn.h"
 #include "attn.h"
 #include "launch.h"
+
+namespace gdn {
+
+namespace {
+constexpr int kMaxDevices = 64;
+}
+
+int sm_count() {
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return sms;
+    if (const int n = known[dev].load(std::memory_order_relaxed)) return n;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+}  // namespace gdn
 
 namespace {
 

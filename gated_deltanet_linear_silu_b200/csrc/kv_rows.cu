@@ -219,12 +219,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowsArgs a, int tb) {
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 template <typename T, int LPR>
 cudaError_t launch_lpr(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
     // whole tokens per CTA: as many (up to 8) as still leave two CTAs for every SM

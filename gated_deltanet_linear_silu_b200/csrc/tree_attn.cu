@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 }
             }
         __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == seg.tiles;
+        const bool whole = seg.whole();
+        if (tid == 0) note_parts(a, seg);
         float* part = partials + (2 * (int)blockIdx.x + seg.later) * slot_floats(D, a.slot_rows);
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), d = 4 * (x % (D / 4));
@@ -533,49 +534,61 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int n = blockIdx.x / a.c.Hk, hk = blockIdx.x % a.c.Hk;
     const int G = a.H / a.c.Hk;
     const int x = blockIdx.y * kWarps + (threadIdx.x >> 5);  // row of the (sequence, head)
-    pdl_wait_previous();
-    const Seq seq = load_seq(a, n);
-    if (x >= seq.nodes * G) return;
     const int rt = x / ROWS, row = x % ROWS;
-    const LineMeta line = line_meta(a)[rt];
-    const int64_t tiles = seq_tiles<TN>(seq);
-    const int64_t start = line_starts(a, rt)[n] + hk * tiles;
-    const int64_t c0 = share_of(start, line.total, line.shares);
-    const int64_t c1 = share_of(start + tiles - 1, line.total, line.shares);
-    if (c0 == c1) return;  // one CTA had the whole unit and wrote it
+    const Seq seq = load_seq(a, n);  // (inputs of the call: not written by the kernel before)
+    pdl_wait_previous();
+    if (x >= seq.nodes * G) return;
+    const UnitParts parts = *unit_parts(a, rt, n, hk);
+    const int c0 = parts.first >> 1, count = parts.last - c0 + 1;
+    // one CTA had the whole unit and wrote it (or the kernel before gave up: then these are anything)
+    if (count < 2 || parts.first < 0 || parts.last >= a.grid) return;
     const float* partials = partial_base(a);
-    auto part = [&](int64_t c) {
-        const bool later = c == c0 && share_start(c0, line.total, line.shares) != start;
-        return partials + (2 * (line.first_cta + c) + later) * slot_floats(D, a.slot_rows);
-    };
-    float mt = kNegInf, lt = 0.f;
-    for (int64_t b = c0; b <= c1; b += 32) mt = fmaxf(mt, b + lane <= c1 ? part(b + lane)[row] : kNegInf);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    auto part = [&](int i) { return partials + (i == 0 ? parts.first : 2 * (c0 + i)) * slot_floats(D, a.slot_rows); };
     constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4s of a lane
-    float4 y[V];
+    constexpr int kAhead = 8 / V;                 // parts whose rows are requested together
+    auto load = [&](int i0, float4 (&z)[kAhead][V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t b = c0; b <= c1; b += 32) {
-        float f = 0.f;
-        if (b + lane <= c1) {
-            const float* p = part(b + lane);
-            const float mi = p[row];
-            f = mi == kNegInf ? 1.f : exp2_approx(mi - mt);  // a part that saw nothing holds zeros (or NaN)
-            lt += p[a.slot_rows + row] * f;
-        }
-        const int count = (int)(c1 - b + 1 < 32 ? c1 - b + 1 : 32);
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            const float* p = part(b + i) + 2 * a.slot_rows + row * D;
+        for (int i = 0; i < kAhead; ++i)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (4 * lane + 128 * v >= D) continue;
-                const float4 z = *reinterpret_cast<const float4*>(p + 4 * lane + 128 * v);
-                y[v].x = fmaf(z.x, fi, y[v].x); y[v].y = fmaf(z.y, fi, y[v].y);
-                y[v].z = fmaf(z.z, fi, y[v].z); y[v].w = fmaf(z.w, fi, y[v].w);
+                z[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < count && 4 * lane + 128 * v < D)
+                    z[i][v] = *reinterpret_cast<const float4*>(part(i0 + i) + 2 * a.slot_rows + row * D + 4 * lane + 128 * v);
             }
+    };
+    float4 z[kAhead][V], y[V];
+    load(0, z);  // beside the references and sums
+    float mt = kNegInf, lt = 0.f, m0 = kNegInf, l0 = 0.f;
+    for (int b = 0; b < count; b += 32)
+        if (b + lane < count) {
+            const float* p = part(b + lane);
+            const float m = p[row];
+            if (b == 0) m0 = m, l0 = p[a.slot_rows + row];
+            mt = fmaxf(mt, m);
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < count; b += 32) {
+        float f = 0.f;
+        if (b + lane < count) {
+            const float* p = part(b + lane);
+            const float m = b == 0 ? m0 : p[row];
+            f = m == kNegInf ? 1.f : exp2_approx(m - mt);  // a part that saw nothing holds zeros (or NaN)
+            lt += (b == 0 ? l0 : p[a.slot_rows + row]) * f;
+        }
+        for (int i = 0; i < 32 && b + i < count; i += kAhead) {
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const float fi = __shfl_sync(0xffffffffu, f, (i + e) & 31);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    y[v].x = fmaf(z[e][v].x, fi, y[v].x); y[v].y = fmaf(z[e][v].y, fi, y[v].y);
+                    y[v].z = fmaf(z[e][v].z, fi, y[v].z); y[v].w = fmaf(z[e][v].w, fi, y[v].w);
+                }
+            }
+            if (b + i + kAhead < count) load(b + i + kAhead, z);
         }
     }
     lt = warp_sum(lt);
@@ -599,11 +612,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     if (a.lse && lane == 0) a.lse[t * a.H + head] = empty ? kNegInf : mt * kLn2 + logf(lt);
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
 
 template <int D>
 int ctas_dim(int e4m3, int rows) {
@@ -614,7 +622,7 @@ int ctas_dim(int e4m3, int rows) {
 // The launch's shape from its sizes alone.
 struct Plan {
     bool tc;  // the tcgen05 kernel
-    int grid, row_tiles, slot_rows, min_tiles;
+    int grid, row_tiles, slot_rows;
 };
 Plan make_plan(int H, int Hk, int D, int max_nodes, int e4m3) {
     Plan p;
@@ -625,8 +633,7 @@ Plan make_plan(int H, int Hk, int D, int max_nodes, int e4m3) {
     p.slot_rows = ((rows < tile ? rows : tile) + 3) / 4 * 4;
     p.grid = sm_count();
     if (!p.tc) p.grid *= D == 64 ? ctas_dim<64>(e4m3, rows) : D == 128 ? ctas_dim<128>(e4m3, rows) : ctas_dim<256>(e4m3, rows);
-    if (p.grid < p.row_tiles) p.grid = p.row_tiles;
-    p.min_tiles = p.tc ? 1 : 2;
+    if (p.grid < p.row_tiles) p.grid = p.row_tiles;  // (every row tile has a CTA)
     return p;
 }
 
@@ -658,16 +665,18 @@ cudaError_t launch_dim(const TreeArgs& a, bool tc, cudaStream_t s) {
 
 size_t tree_workspace_bytes(int N, int H, int Hk, int D, int max_nodes, int e4m3) {
     const Plan p = make_plan(H, Hk, D, max_nodes, e4m3);
-    return meta_bytes(p.row_tiles, N) + 2 * (size_t)p.grid * slot_floats(D, p.slot_rows) * sizeof(float);
+    return units_bytes(p.row_tiles, N, Hk) + 2 * (size_t)p.grid * slot_floats(D, p.slot_rows) * sizeof(float);
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
     TreeArgs a = args;
     const Plan p = make_plan(a.H, a.c.Hk, a.c.D, a.max_nodes, a.c.e4m3);
-    a.grid = p.grid;
+    // no more CTAs than the tables have room for tiles
+    const int64_t tiles = ((((int64_t)a.p.max_pages << a.c.page_shift) + kTile - 1) / kTile) * a.p.N * a.c.Hk * p.row_tiles;
+    a.grid = tiles < p.grid ? (int)tiles : p.grid;
+    if (a.grid < p.row_tiles) a.grid = p.row_tiles;
     a.row_tiles = p.row_tiles;
     a.slot_rows = p.slot_rows;
-    a.min_tiles = p.min_tiles;
     return a.c.D == 64 ? launch_dim<64>(a, p.tc, s) : a.c.D == 128 ? launch_dim<128>(a, p.tc, s) : launch_dim<256>(a, p.tc, s);
 }
 

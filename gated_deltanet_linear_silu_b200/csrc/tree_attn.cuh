@@ -117,26 +117,29 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int n) {
     return q;
 }
 
-// One row tile's line, in the workspace for the joining kernel.
-struct LineMeta {
-    int64_t total, shares, first_cta;
+// Workspace: for every unit ([row_tiles][N * Hk]) where its partials are; per
+// CTA two partials (of the segment at the start of its stretch, and of one that
+// starts later), each m, l [slot_rows] and o [slot_rows][D].
+struct UnitParts {
+    int first;  // partial of the unit's first segment: 2 CTA + (0 or 1)
+    int last;   // CTA of its last one; the CTAs between have theirs at 2 CTA
 };
-
-// Workspace: LineMeta [row_tiles]; the start of every sequence on every line,
-// int64 [row_tiles][N]; per CTA two partials (of the segment at the start of
-// its stretch, and of one that starts later), each m, l [slot_rows] and o
-// [slot_rows][D].
-__host__ __device__ inline size_t meta_bytes(int row_tiles, int N) {
-    return (sizeof(LineMeta) * row_tiles + (size_t)row_tiles * N * 8 + 255) / 256 * 256;
+__host__ __device__ inline size_t units_bytes(int row_tiles, int N, int Hk) {
+    return (sizeof(UnitParts) * row_tiles * N * Hk + 255) / 256 * 256;
 }
 __host__ __device__ inline size_t slot_floats(int D, int slot_rows) { return (size_t)slot_rows * (D + 2); }
 
-__device__ __forceinline__ LineMeta* line_meta(const TreeArgs& a) { return static_cast<LineMeta*>(a.workspace); }
-__device__ __forceinline__ int64_t* line_starts(const TreeArgs& a, int rt) {
-    return reinterpret_cast<int64_t*>(line_meta(a) + a.row_tiles) + (int64_t)rt * a.p.N;
+__device__ __forceinline__ UnitParts* unit_parts(const TreeArgs& a, int rt, int n, int hk) {
+    return static_cast<UnitParts*>(a.workspace) + ((int64_t)rt * a.p.N + n) * a.c.Hk + hk;
 }
 __device__ __forceinline__ float* partial_base(const TreeArgs& a) {
-    return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + meta_bytes(a.row_tiles, a.p.N));
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + units_bytes(a.row_tiles, a.p.N, a.c.Hk));
+}
+
+// a / b of non-negative numbers: 64-bit division is a long call, and these
+// mostly fit 32.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <int ROWS>
@@ -155,13 +158,7 @@ struct Share {
     int rt, n;
 };
 
-__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t shares) { return c * total / shares; }
-__device__ __forceinline__ int64_t share_of(int64_t tile, int64_t total, int64_t shares) {
-    return ((tile + 1) * shares - 1) / total;  // the c with share_start(c) <= tile < share_start(c + 1)
-}
-
-// Every thread of the CTA takes part (it synchronises the CTA). The first CTA
-// of each row tile also writes that line's data to the workspace.
+// Every thread of the CTA takes part (it synchronises the CTA).
 template <int ROWS, int TN, int THREADS>
 __device__ __forceinline__ Share find_share(const TreeArgs& a) {
     constexpr int W = THREADS / 32;
@@ -191,35 +188,22 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
     s.rt = RT;
     s.n = N;
     s.n_start = 0;
-    int64_t shares = 0, total = 0;
-    int cta = 0;
-    bool first_cta = false;
     {
         int64_t line = run;  // line 0
-        for (int rt = 0; rt < RT; ++rt) {
-            int64_t count = line > 0 ? 1 + ((int64_t)gridDim.x - active) * line / all : 0;
-            int64_t sh = line / a.min_tiles;
-            sh = sh < 1 ? 1 : sh < count ? sh : count;
-            if (line == 0) sh = 0;
-            if (blockIdx.x == 0 && tid == 0) line_meta(a)[rt] = LineMeta{line, sh, cta};
-            const bool here = blockIdx.x >= (unsigned)cta && blockIdx.x < (unsigned)(cta + count);
-            if (here) {
+        int cta = 0;
+        for (int rt = 0; rt < RT && line > 0; ++rt) {
+            const int64_t count = 1 + quotient(((int64_t)gridDim.x - active) * line, all);
+            const int64_t shares = line < count ? line : count;
+            const int64_t c = (int64_t)blockIdx.x - cta;
+            if (c >= 0 && c < shares) {
                 s.rt = rt;
-                shares = sh;
-                total = line;
-                first_cta = blockIdx.x == (unsigned)cta;
-                const int64_t c = blockIdx.x - cta;
-                if (c < sh) {
-                    s.begin = share_start(c, line, sh);
-                    s.end = share_start(c + 1, line, sh);
-                }
+                s.begin = quotient(c * line, shares);
+                s.end = quotient((c + 1) * line, shares);
             }
             cta += (int)count;
             line -= (int64_t)totals[rt];
         }
     }
-    (void)total;
-    (void)shares;
     if (s.begin == s.end) return s;
     int64_t before = 0;
     for (int n0 = 0; n0 < N; n0 += THREADS) {
@@ -243,13 +227,12 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
             before += scan[w];
         }
         const int64_t start = pre + x - own;
-        if (first_cta && n < N) line_starts(a, s.rt)[n] = start;
         if (start <= s.begin && s.begin < start + own) {
             found[0] = n;
             found[1] = start;
         }
         __syncthreads();
-        if (!first_cta && found[0] < N) break;
+        if (found[0] < N) break;
     }
     s.n = (int)found[0];
     s.n_start = found[1];
@@ -262,13 +245,14 @@ struct Segment {
     int n, hk, rt, rows;      // rows: query rows of this row tile
     int tile0, tile1, tiles;  // its token tiles, of the unit's
     int later;                // 0: it starts where the stretch starts
+    __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
     int64_t n_start, end;     // of the sequence and of this segment, on the line
 };
 
 template <int ROWS, int TN>
 __device__ __forceinline__ void place_segment(const TreeArgs& a, const Share& s, int64_t at, Segment& g) {
     g.tiles = (int)seq_tiles<TN>(g.seq);
-    const int64_t unit = (at - g.n_start) / g.tiles, unit_start = g.n_start + unit * g.tiles;
+    const int64_t unit = quotient(at - g.n_start, g.tiles), unit_start = g.n_start + unit * g.tiles;
     g.hk = (int)unit;
     g.tile0 = (int)(at - unit_start);
     g.tile1 = (int)(s.end - unit_start < g.tiles ? s.end - unit_start : g.tiles);
@@ -298,6 +282,13 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, const Share& s, 
     }
     place_segment<ROWS, TN>(a, s, at, g);
     return true;
+}
+
+// Tells the joining kernel where a unit's partials are (one thread per segment).
+__device__ __forceinline__ void note_parts(const TreeArgs& a, const Segment& g) {
+    UnitParts* u = unit_parts(a, g.rt, g.n, g.hk);
+    if (g.tile0 == 0) u->first = 2 * (int)blockIdx.x + g.later;
+    if (g.tile1 == g.tiles) u->last = (int)blockIdx.x;
 }
 
 }  // namespace gdn

@@ -776,7 +776,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 }
                 l = row_sum[m] * f_0 + row_sum[128 + m] * f_1;
                 const bool have_0 = !C::kGroups || tiles > 1 || !(i0 & 1), have_1 = C::kGroups && (tiles > 1 || (i0 & 1));
-                const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
+                const bool whole = seg.whole();
+                if (tid == 0) note_parts(a, seg);
                 const bool empty = ref == kNegInf && l == 0.f;
                 const float inv = empty ? 0.f : 1.f / l;
                 const int64_t out = (t * a.H + head) * D;
