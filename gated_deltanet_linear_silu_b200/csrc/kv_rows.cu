@@ -8,13 +8,17 @@
 //                                                     elements, angle pos * inv_freq
 //   e4m3 row: scale = amax / 448, code = x / scale    nearest even
 //
-// All of it is HBM-bound (each element read once, written once); a row is held
-// by a group of D / 8 lanes, eight elements each, so that a bf16 row moves in
-// 16-byte vectors and the norm and amax are shuffles within the group. The
-// sine and cosine of a token serve all its heads: a CTA takes whole tokens and
-// computes them once into shared memory. The angle's turns, pos * inv_freq /
-// (2 pi), are taken in fp64 and reduced to [-1/2, 1/2] there: in fp32 a
-// position of 2^18 would lose 2^-6 of a radian.
+// All of it is HBM-bound (each element read once, written once) if few
+// instructions go with a 16-byte piece. A warp takes one token (or a share of
+// its heads, where tokens are few) and walks its heads, 32 / LPR rows at a time,
+// LPR lanes of eight elements to a row: the norm and amax are shuffles within
+// the lane group, and the token's place in the cache, its angles and the
+// weights are looked up once for all its heads. Where pairs are the two halves
+// of the rotated part, a lane of that part takes four elements of either half,
+// so that a pair stays in one lane and the rotation exchanges nothing.
+//
+// The angle's turns, pos * inv_freq / (2 pi), are taken in fp64 and reduced to
+// [-1/2, 1/2] there: in fp32 a position of 2^18 would lose 2^-6 of a radian.
 #include <cfloat>
 
 #include "kv_page.cuh"
@@ -23,54 +27,55 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBatch = 4;  // rows of a lane group in flight
-constexpr int kMaxTokens = 8;  // tokens of a CTA
+constexpr int kBatch = 4;  // row groups of a warp in flight
 
-template <typename T> struct Vec8;
-template <> struct Vec8<uint16_t> {
-    uint4 u;
-    __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+// Four consecutive elements, as loaded.
+template <typename T> struct Vec4;
+template <> struct Vec4<uint16_t> {
+    uint2 u;
+    __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = __uint_as_float(u.x << 16);
+        x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(u.y << 16);
+        x[3] = __uint_as_float(u.y & 0xFFFF0000u);
     }
 };
-template <> struct Vec8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p + 4));
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+template <> struct Vec4<float> {
+    float4 f;
+    __device__ __forceinline__ void load(const float* p) { f = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
     }
 };
-__device__ __forceinline__ void put8(uint16_t* p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint2 bf16x4(const float* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void put8(float* p, const float (&x)[8]) {
+__device__ __forceinline__ void put4(uint16_t* p, const float* x) { *reinterpret_cast<uint2*>(p) = bf16x4(x); }
+__device__ __forceinline__ void put4(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+// Eight elements in two runs of four at p0 and p1; one store where they meet.
+template <typename T>
+__device__ __forceinline__ void put44(T* row, int p0, int p1, const float (&x)[8]) {
+    if (sizeof(T) == 2 && p1 == p0 + 4) {
+        const uint2 a = bf16x4(x), b = bf16x4(x + 4);
+        *reinterpret_cast<uint4*>(row + p0) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+        put4(row + p0, x);
+        put4(row + p1, x + 4);
+    }
 }
 
 // Stores one row's eight elements per lane in the cache; every lane of the
 // group takes part (the amax is the group's). A row with an element that is
 // not finite is stored as scale NaN: it reads back as NaN.
 template <int LPR>
-__device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t row, int l, bool on, float (&x)[8]) {
+__device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t row, int l, int p0, int p1, bool on,
+                                          float (&x)[8]) {
     if (!c.e4m3) {
-        if (on) put8(static_cast<uint16_t*>(is_v ? c.v : c.k) + row * c.D + 8 * l, x);
+        if (on) put44(static_cast<uint16_t*>(is_v ? c.v : c.k) + row * c.D, p0, p1, x);
         return;
     }
     uint32_t m = 0;  // bits of |x| order as the values do, with inf and NaN on top
@@ -80,156 +85,175 @@ __device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t
     for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool finite = m < 0x7F800000u;
     const float scale = finite ? __uint_as_float(m) / 448.f : __uint_as_float(0x7FC00000u);
-    const bool zero = !finite || scale == 0.f;
+    if (finite && m > 0x0D800000u) {
+        // The quotient rounded once (Markstein): with r the reciprocal rounded to
+        // nearest, q + r (x - q s), q = x r, rounds to x / s wherever no step leaves the
+        // normal range -- here quotients are at most 448 and s is above 2^-109.
+        const float r = 1.f / scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : x[i] / scale;
+        for (int i = 0; i < 8; ++i) {
+            const float q = x[i] * r;
+            x[i] = fmaf(fmaf(-q, scale, x[i]), r, q);
+        }
+    } else {
+        const bool zero = !finite || scale == 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : x[i] / scale;
+    }
     if (!on) return;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + row * c.D + 8 * l) = to_e4m3x8(x);
+    const uint2 codes = to_e4m3x8(x);
+    uint8_t* p = static_cast<uint8_t*>(is_v ? c.v : c.k) + row * c.D;
+    if (p1 == p0 + 4) {
+        *reinterpret_cast<uint2*>(p + p0) = codes;
+    } else {
+        *reinterpret_cast<uint32_t*>(p + p0) = codes.x;
+        *reinterpret_cast<uint32_t*>(p + p1) = codes.y;
+    }
     if (l == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
 }
 
-// One CTA: tb tokens, all their rows (q then k then v heads of each token).
+// Groups of 32 / LPR rows of a token: queries, keys, values. `share` warps take
+// a token's groups in turn.
 template <typename T, int LPR, int MODE>
-__global__ void __launch_bounds__(kThreads) rows_kernel(RowsArgs a, int tb) {
-    extern __shared__ float trig[];  // cos [tb][half], then sin [tb][half]
-    __shared__ int64_t where[kMaxTokens];
-    constexpr int RW = 32 / LPR;  // rows of a warp's pass
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kThreads) rows_kernel(RowsArgs a, int share_shift) {
+    extern __shared__ float trig[];  // per warp: cos [half], sin [half]
+    constexpr int RW = 32 / LPR;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, sub = lane / LPR;
     const int D = a.D, half = a.rotary >> 1;
     const bool on = 8 * l < D;
-    const int H = MODE == kCacheWrite ? 0 : a.H;
-    const int R = H + (MODE == kNormRope ? a.Hk : 2 * a.Hk);
-    const int64_t t0 = (int64_t)blockIdx.x * tb;
-    const int nt = (int)(a.T - t0 < tb ? a.T - t0 : tb);
-    const int rows = nt * R;
-    constexpr int kStep = kWarps * RW;
+    const int64_t gw = (int64_t)blockIdx.x * kWarps + warp, t = gw >> share_shift;
+    const int part = (int)(gw & ((1 << share_shift) - 1));
+    if (t >= a.T) return;
+    const int nq = MODE == kCacheWrite ? 0 : (a.H + RW - 1) / RW, nk = (a.Hk + RW - 1) / RW;
+    const int groups = nq + (MODE == kNormRope ? nk : 2 * nk);
+    // this lane's elements of a normed row
+    const bool turned = MODE != kCacheWrite && 8 * l < a.rotary;
+    const bool split = turned && !a.interleaved;
+    const int p0 = split ? 4 * l : 8 * l, p1 = split ? half + 4 * l : 8 * l + 4;
 
-    // Token and head slot of row r, and its load.
-    Vec8<T> raw[kBatch];
-    auto load = [&](int r0) {
+    Vec4<T> raw[kBatch][2];
+    auto load = [&](int g0) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u * kStep + warp * RW + sub;
-            if (r >= rows || !on) continue;
-            const int64_t t = t0 + r / R;
-            const int j = r % R;
-            const T* src = j < H ? static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)j * D
-                         : j < H + a.Hk ? static_cast<const T*>(a.k) + t * a.ld_k + (int64_t)(j - H) * D
-                                        : static_cast<const T*>(a.v) + t * a.ld_v + (int64_t)(j - H - a.Hk) * D;
-            raw[u].load(src + 8 * l);
+            const int g = g0 + (u << share_shift);
+            if (g >= groups) break;
+            const bool is_q = g < nq, is_v = g >= nq + nk;
+            const int j = (is_q ? g : is_v ? g - nq - nk : g - nq) * RW + sub;
+            if (!on || j >= (is_q ? a.H : a.Hk)) continue;
+            const T* src = (is_q ? static_cast<const T*>(a.q) + t * a.ld_q
+                            : is_v ? static_cast<const T*>(a.v) + t * a.ld_v
+                                   : static_cast<const T*>(a.k) + t * a.ld_k) + (int64_t)j * D;
+            raw[u][0].load(src + (is_v ? 8 * l : p0));
+            raw[u][1].load(src + (is_v ? 8 * l + 4 : p1));
         }
     };
-    load(0);
-    if (MODE != kNormRope && tid < nt) {
-        const int64_t row = token_row(a.p, a.c, t0 + tid);
-        where[tid] = row;
-        if (row == kRowBad) set_status(a.status, kStatusBadSeqlens);
-    }
-    float wq[8], wk[8];
+    load(part);
+    float wq[8], wk[8], cs[4], sn[4];
     if (MODE != kCacheWrite) {
-        for (int i = tid; i < nt * half; i += kThreads) {
-            const double turns = (double)a.pos[t0 + i / half] * a.inv_freq[i % half] * 0.15915494309189533577;
-            float s, c;
-            sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-            trig[i] = c;
-            trig[tb * half + i] = s;
+        float* cw = trig + warp * 2 * half;
+        const double pos = (double)a.pos[t] * 0.15915494309189533577;  // 1 / (2 pi)
+        for (int i = lane; i < half; i += 32) {
+            const double turns = pos * a.inv_freq[i];
+            sincospif(2.f * (float)(turns - rint(turns)), &cw[half + i], &cw[i]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = turned ? cw[4 * l + e] : 1.f;
+            sn[e] = turned ? cw[half + 4 * l + e] : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            wq[i] = on ? a.q_w[8 * l + i] : 0.f;
-            wk[i] = on ? a.k_w[8 * l + i] : 0.f;
+        for (int e = 0; e < 8; ++e) {
+            const int p = e < 4 ? p0 + e : p1 + e - 4;
+            wq[e] = on ? a.q_w[p] : 0.f;
+            wk[e] = on ? a.k_w[p] : 0.f;
         }
     }
-    __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += kBatch * kStep) {
-        if (r0 > 0) load(r0);
+    int64_t where = 0;
+    if (MODE != kNormRope) {
+        where = token_row(a.p, a.c, t);
+        if (where < 0) {
+            if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
+            return;
+        }
+    }
+    auto normed = [&](float (&x)[8], const float (&w)[8]) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = 1.f / sqrtf(ss / (float)D + a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+        if (!turned) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // (every index a constant: x stays in registers)
+            const float p = a.interleaved ? x[2 * e] : x[e], q = a.interleaved ? x[2 * e + 1] : x[e + 4];
+            const float y = p * cs[e] - q * sn[e], z = q * cs[e] + p * sn[e];
+            if (a.interleaved) {
+                x[2 * e] = y;
+                x[2 * e + 1] = z;
+            } else {
+                x[e] = y;
+                x[e + 4] = z;
+            }
+        }
+    };
+    for (int g0 = part; g0 < groups; g0 += kBatch << share_shift) {
+        if (g0 != part) load(g0);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int rw = r0 + u * kStep + warp * RW;  // first row of the warp's pass
-            if (rw >= rows) break;
-            const int r = rw + sub;
-            const bool live = r < rows;
-            const int i = live ? r / R : 0, j = live ? r % R : 0;
+            const int g = g0 + (u << share_shift);
+            if (g >= groups) break;
+            const bool is_q = g < nq, is_v = g >= nq + nk;
+            const int j = (is_q ? g : is_v ? g - nq - nk : g - nq) * RW + sub;
+            const bool live = on && j < (is_q ? a.H : a.Hk);
             float x[8];
-            if (live && on) raw[u].get(x);
-            else
+            if (live) {
+                raw[u][0].get(x);
+                raw[u][1].get(x + 4);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            if (MODE != kCacheWrite) {
-                const bool normed = j < H + a.Hk;
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float inv = 1.f / sqrtf(ss / (float)D + a.eps);
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] * inv * (j < H ? wq[e] : wk[e]);
-                const int c0 = 8 * l;
-                const bool turned = c0 < a.rotary;
-                const float* cs = trig + i * half;
-                const float* sn = cs + tb * half;
-                if (a.interleaved) {
-                    if (turned) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const float c = cs[(c0 + e) >> 1], s = sn[(c0 + e) >> 1];
-                            const float p = y[e], q = y[e + 1];
-                            y[e] = p * c - q * s;
-                            y[e + 1] = q * c + p * s;
-                        }
-                    }
-                } else {
-                    // the pair's other element sits half / 8 lanes away (rotary is a multiple of 16)
-                    const bool first = c0 < half;
-                    const int peer = turned ? (first ? lane + half / 8 : lane - half / 8) : lane;
-                    const int at = turned ? (first ? c0 : c0 - half) : 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float p = __shfl_sync(0xffffffffu, y[e], peer);
-                        if (turned) y[e] = y[e] * cs[at + e] + (first ? -p : p) * sn[at + e];
-                    }
-                }
-                if (normed) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = y[e];
-                }
             }
+            if (MODE != kCacheWrite && is_q) {
+                normed(x, wq);
+                if (live) put44(static_cast<T*>(a.q_out) + (t * a.H + j) * D, p0, p1, x);
+                continue;
+            }
+            if (MODE != kCacheWrite && !is_v) normed(x, wk);
             if (MODE == kNormRope) {
-                if (live && on) {
-                    const int64_t t = t0 + i;
-                    T* dst = j < H ? static_cast<T*>(a.q_out) + (t * H + j) * D
-                                   : static_cast<T*>(a.k_out) + (t * a.Hk + j - H) * D;
-                    put8(dst + 8 * l, x);
-                }
+                if (live) put44(static_cast<T*>(a.k_out) + (t * a.Hk + j) * D, p0, p1, x);
             } else {
-                const int64_t row = live ? where[i] : kRowNone;
-                const bool store = row >= 0 && on;
-                if (MODE == kNormRopeCache && j < H && store)
-                    put8(static_cast<T*>(a.q_out) + ((t0 + i) * H + j) * D + 8 * l, x);
-                const int hk = j - H;
-                if (!__any_sync(0xffffffffu, hk >= 0)) continue;  // queries only
-                const bool is_v = hk >= a.Hk;
-                put_cache<LPR>(a.c, is_v, row + ((int64_t)(is_v ? hk - a.Hk : hk) << a.c.page_shift), l,
-                               store && hk >= 0, x);
+                put_cache<LPR>(a.c, is_v, where + ((int64_t)j << a.c.page_shift), l, is_v ? 8 * l : p0,
+                               is_v ? 8 * l + 4 : p1, live, x);
             }
         }
     }
+}
+
+// Warps to a token (log2): more while the GPU would not be full without them.
+int share_of_token(int64_t T, int groups) {
+    int s = 0;
+    while (s < 3 && (T << s) < 2 * kWarps * (int64_t)sm_count() && (2 << s) <= groups) ++s;
+    return s;
 }
 
 template <typename T, int LPR>
 cudaError_t launch_lpr(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
-    // whole tokens per CTA: as many (up to 8) as still leave two CTAs for every SM
-    int tb = kMaxTokens;
-    while (tb > 1 && (a.T + tb - 1) / tb < 2 * sm_count()) tb >>= 1;
-    const unsigned grid = (unsigned)((a.T + tb - 1) / tb);
-    const size_t smem = mode == kCacheWrite ? 0 : sizeof(float) * tb * a.rotary;
+    constexpr int RW = 32 / LPR;
+    const int nk = (a.Hk + RW - 1) / RW;
+    const int groups = mode == kCacheWrite ? 2 * nk : (a.H + RW - 1) / RW + (mode == kNormRope ? nk : 2 * nk);
+    const int share = share_of_token(a.T, groups);
+    const unsigned grid = (unsigned)(((a.T << share) + kWarps - 1) / kWarps);
+    const size_t smem = mode == kCacheWrite ? 0 : sizeof(float) * kWarps * a.rotary;
     switch (mode) {
-        case kNormRope: rows_kernel<T, LPR, kNormRope><<<grid, kThreads, smem, s>>>(a, tb); break;
-        case kNormRopeCache: rows_kernel<T, LPR, kNormRopeCache><<<grid, kThreads, smem, s>>>(a, tb); break;
-        case kCacheWrite: rows_kernel<T, LPR, kCacheWrite><<<grid, kThreads, smem, s>>>(a, tb); break;
+        case kNormRope: rows_kernel<T, LPR, kNormRope><<<grid, kThreads, smem, s>>>(a, share); break;
+        case kNormRopeCache: rows_kernel<T, LPR, kNormRopeCache><<<grid, kThreads, smem, s>>>(a, share); break;
+        case kCacheWrite: rows_kernel<T, LPR, kCacheWrite><<<grid, kThreads, smem, s>>>(a, share); break;
     }
     return cudaGetLastError();
 }
@@ -243,63 +267,87 @@ cudaError_t launch_type(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
     return launch_lpr<T, 32>(a, mode, s);
 }
 
-// ---- reading back: a CTA takes 16 tokens (one page's run, where pages are that
-// long), a lane eight elements of a row.
-constexpr int kReadTokens = 16;
-
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a) {
-    __shared__ int64_t where[kReadTokens];
-    const int tid = threadIdx.x, D = a.c.D, Hk = a.c.Hk, cols = D >> 3;
-    const int64_t t0 = (int64_t)blockIdx.x * kReadTokens;
-    const int nt = (int)(a.T - t0 < kReadTokens ? a.T - t0 : kReadTokens);
-    if (tid < nt) {
-        const int64_t row = token_row(a.p, a.c, t0 + tid);
-        where[tid] = row;
-        if (row == kRowBad) set_status(a.status, kStatusBadSeqlens);
+// ---- reading back, the same walk: key rows, then value rows of a token.
+template <typename T, int LPR, bool E4M3>
+__global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a, int share_shift) {
+    constexpr int RW = 32 / LPR, kAhead = 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int l = lane % LPR, sub = lane / LPR;
+    const int D = a.c.D, Hk = a.c.Hk;
+    const bool on = 8 * l < D;
+    const int64_t gw = (int64_t)blockIdx.x * kWarps + warp, t = gw >> share_shift;
+    const int part = (int)(gw & ((1 << share_shift) - 1));
+    if (t >= a.T) return;
+    const int64_t where = token_row(a.p, a.c, t);
+    if (where < 0) {
+        if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
+        return;
     }
-    __syncthreads();
-    const bool is_v = blockIdx.y != 0;
-    const uint8_t* src = static_cast<const uint8_t*>(is_v ? a.c.v : a.c.k);
-    const float* scales = is_v ? a.c.v_scale : a.c.k_scale;
-    T* dst = static_cast<T*>(is_v ? a.v : a.k) + t0 * Hk * D;
-    const int items = nt * Hk * cols;
-    for (int x0 = tid; x0 < items; x0 += kBatch * kThreads) {
-        uint4 raw[kBatch];
-        float sc[kBatch];
+    const int nk = (Hk + RW - 1) / RW;
+    for (int g0 = part; g0 < 2 * nk; g0 += kAhead << share_shift) {
+        uint4 raw[kAhead];
+        float sc[kAhead];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int x = x0 + u * kThreads;
-            if (x >= items) break;
-            const int r = x / cols, e = 8 * (x - r * cols), i = r / Hk;
-            if (where[i] < 0) continue;
-            const int64_t row = where[i] + ((int64_t)(r - i * Hk) << a.c.page_shift);
+        for (int u = 0; u < kAhead; ++u) {
+            const int g = g0 + (u << share_shift);
+            if (g >= 2 * nk) break;
+            const int j = (g < nk ? g : g - nk) * RW + sub;
+            if (!on || j >= Hk) continue;
+            const int64_t row = where + ((int64_t)j << a.c.page_shift);
+            const uint8_t* src = static_cast<const uint8_t*>(g < nk ? a.c.k : a.c.v);
             if (E4M3) {
-                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src + row * D + e));
+                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src + row * D + 8 * l));
                 raw[u] = make_uint4(w.x, w.y, 0, 0);
-                sc[u] = scales[row];
+                sc[u] = __ldg((g < nk ? a.c.k_scale : a.c.v_scale) + row);
             } else {
-                raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + 2 * (row * D + e)));
+                raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + 2 * (row * D + 8 * l)));
             }
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int x = x0 + u * kThreads;
-            if (x >= items) break;
-            if (where[x / cols / Hk] < 0) continue;
+        for (int u = 0; u < kAhead; ++u) {
+            const int g = g0 + (u << share_shift);
+            if (g >= 2 * nk) break;
+            const int j = (g < nk ? g : g - nk) * RW + sub;
+            if (!on || j >= Hk) continue;
+            T* dst = static_cast<T*>(g < nk ? a.k : a.v) + (t * Hk + j) * D;
             float f[8];
             if (E4M3) {
                 from_e4m3x8(make_uint2(raw[u].x, raw[u].y), f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= sc[u];
+            } else if (sizeof(T) == 2) {
+                *reinterpret_cast<uint4*>(dst + 8 * l) = raw[u];
+                continue;
             } else {
-                Vec8<uint16_t> b;
-                b.u = raw[u];
-                b.get(f);
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(w[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                }
             }
-            put8(dst + 8 * (int64_t)x, f);
+            put44(dst, 8 * l, 8 * l + 4, f);
         }
     }
+}
+
+template <typename T, int LPR>
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
+    constexpr int RW = 32 / LPR;
+    const int share = share_of_token(a.T, 2 * ((a.c.Hk + RW - 1) / RW));
+    const unsigned grid = (unsigned)(((a.T << share) + kWarps - 1) / kWarps);
+    if (a.c.e4m3) read_kernel<T, LPR, true><<<grid, kThreads, 0, s>>>(a, share);
+    else read_kernel<T, LPR, false><<<grid, kThreads, 0, s>>>(a, share);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_read_type(const ReadArgs& a, cudaStream_t s) {
+    if (a.c.D <= 16) return launch_read<T, 2>(a, s);
+    if (a.c.D <= 32) return launch_read<T, 4>(a, s);
+    if (a.c.D <= 64) return launch_read<T, 8>(a, s);
+    if (a.c.D <= 128) return launch_read<T, 16>(a, s);
+    return launch_read<T, 32>(a, s);
 }
 
 // ---- accepting a path: one CTA per sequence. Row base + a takes row base +
@@ -376,15 +424,7 @@ cudaError_t launch_rows(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
 
 cudaError_t launch_kv_read(const ReadArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
-    const dim3 grid((unsigned)((a.T + kReadTokens - 1) / kReadTokens), 2);
-    if (a.out_bf16) {
-        if (a.c.e4m3) read_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-        else read_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (a.c.e4m3) read_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
-        else read_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    return a.out_bf16 ? launch_read_type<uint16_t>(a, s) : launch_read_type<float>(a, s);
 }
 
 cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s) {
