@@ -71,6 +71,7 @@ gdn_status_t check_norm(int H, int Hk, int D, const float* q_w, const float* k_w
     if (!row_dim_ok(D)) return GDN_ERR_UNSUPPORTED;
     if (rotary < 0 || rotary > D) return GDN_ERR_INVALID_ARG;
     if (rotary % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(q_w, 16) || !aligned(k_w, 16)) return GDN_ERR_INVALID_ARG;
     if (!q_w || !k_w || !pos || (rotary > 0 && !inv_freq)) return GDN_ERR_INVALID_ARG;
     return GDN_OK;
 }

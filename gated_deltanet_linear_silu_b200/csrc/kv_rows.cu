@@ -68,6 +68,20 @@ __device__ __forceinline__ void put44(T* row, int p0, int p1, const float (&x)[8
     }
 }
 
+// x / s rounded once, given r close to 1 / s (Markstein's correction: the
+// remainder of x r, times r, added to it). Where the quotient is a number of the
+// format -- the ties of the rounding that follows among them -- it comes out
+// exactly. No step may leave the normal range.
+__device__ __forceinline__ float corrected(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+__device__ __forceinline__ float reciprocal(float s) {  // within an ulp, for normal s: one Newton step
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+
 // Stores one row's eight elements per lane in the cache; every lane of the
 // group takes part (the amax is the group's). A row with an element that is
 // not finite is stored as scale NaN: it reads back as NaN.
@@ -83,22 +97,18 @@ __device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool finite = m < 0x7F800000u;
-    const float scale = finite ? __uint_as_float(m) / 448.f : __uint_as_float(0x7FC00000u);
-    if (finite && m > 0x0D800000u) {
-        // The quotient rounded once (Markstein): with r the reciprocal rounded to
-        // nearest, q + r (x - q s), q = x r, rounds to x / s wherever no step leaves the
-        // normal range -- here quotients are at most 448 and s is above 2^-109.
-        const float r = 1.f / scale;
+    float scale;
+    if (m - 0x0D800000u < 0x72000000u - 0x0D800000u) {  // 2^-100 <= amax < 2^101
+        scale = corrected(__uint_as_float(m), 448.f, 1.f / 448.f);
+        const float r = reciprocal(scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = x[i] * r;
-            x[i] = fmaf(fmaf(-q, scale, x[i]), r, q);
-        }
+        for (int i = 0; i < 8; ++i) x[i] = corrected(x[i], scale, r);
     } else {
+        const bool finite = m < 0x7F800000u;
+        scale = finite ? __uint_as_float(m) / 448.f : __uint_as_float(0x7FC00000u);
         const bool zero = !finite || scale == 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : x[i] / scale;
+        for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : __fdiv_rn(x[i], scale);
     }
     if (!on) return;
     const uint2 codes = to_e4m3x8(x);
@@ -112,124 +122,142 @@ __device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t
     if (l == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
 }
 
-// Groups of 32 / LPR rows of a token: queries, keys, values. `share` warps take
-// a token's groups in turn.
-template <typename T, int LPR, int MODE>
-__global__ void __launch_bounds__(kThreads) rows_kernel(RowsArgs a, int share_shift) {
+// Groups of 32 / LPR rows of a token: queries, keys, values. 1 << share_shift
+// warps take a token's groups in turn; INTER: pairs are neighbours.
+template <typename T, int LPR, int MODE, bool INTER>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(RowsArgs a, int share_shift) {
     extern __shared__ float trig[];  // per warp: cos [half], sin [half]
     constexpr int RW = 32 / LPR;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, sub = lane / LPR;
     const int D = a.D, half = a.rotary >> 1;
     const bool on = 8 * l < D;
-    const int64_t gw = (int64_t)blockIdx.x * kWarps + warp, t = gw >> share_shift;
+    const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
     const int part = (int)(gw & ((1 << share_shift) - 1));
-    if (t >= a.T) return;
     const int nq = MODE == kCacheWrite ? 0 : (a.H + RW - 1) / RW, nk = (a.Hk + RW - 1) / RW;
     const int groups = nq + (MODE == kNormRope ? nk : 2 * nk);
     // this lane's elements of a normed row
     const bool turned = MODE != kCacheWrite && 8 * l < a.rotary;
-    const bool split = turned && !a.interleaved;
+    const bool split = turned && !INTER;
     const int p0 = split ? 4 * l : 8 * l, p1 = split ? half + 4 * l : 8 * l + 4;
-
-    Vec4<T> raw[kBatch][2];
-    auto load = [&](int g0) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int g = g0 + (u << share_shift);
-            if (g >= groups) break;
-            const bool is_q = g < nq, is_v = g >= nq + nk;
-            const int j = (is_q ? g : is_v ? g - nq - nk : g - nq) * RW + sub;
-            if (!on || j >= (is_q ? a.H : a.Hk)) continue;
-            const T* src = (is_q ? static_cast<const T*>(a.q) + t * a.ld_q
-                            : is_v ? static_cast<const T*>(a.v) + t * a.ld_v
-                                   : static_cast<const T*>(a.k) + t * a.ld_k) + (int64_t)j * D;
-            raw[u][0].load(src + (is_v ? 8 * l : p0));
-            raw[u][1].load(src + (is_v ? 8 * l + 4 : p1));
-        }
-    };
-    load(part);
-    float wq[8], wk[8], cs[4], sn[4];
+    const float inv_d = 1.f / (float)D;
+    float wq[8], wk[8];
     if (MODE != kCacheWrite) {
-        float* cw = trig + warp * 2 * half;
-        const double pos = (double)a.pos[t] * 0.15915494309189533577;  // 1 / (2 pi)
-        for (int i = lane; i < half; i += 32) {
-            const double turns = pos * a.inv_freq[i];
-            sincospif(2.f * (float)(turns - rint(turns)), &cw[half + i], &cw[i]);
-        }
-        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            cs[e] = turned ? cw[4 * l + e] : 1.f;
-            sn[e] = turned ? cw[half + 4 * l + e] : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int p = e < 4 ? p0 + e : p1 + e - 4;
-            wq[e] = on ? a.q_w[p] : 0.f;
-            wk[e] = on ? a.k_w[p] : 0.f;
+        for (int e = 0; e < 8; e += 4) {
+            const int p = e ? p1 : p0;
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 x = on ? *reinterpret_cast<const float4*>(a.q_w + p) : z;
+            const float4 y = on ? *reinterpret_cast<const float4*>(a.k_w + p) : z;
+            wq[e] = x.x; wq[e + 1] = x.y; wq[e + 2] = x.z; wq[e + 3] = x.w;
+            wk[e] = y.x; wk[e + 1] = y.y; wk[e + 2] = y.z; wk[e + 3] = y.w;
         }
     }
-    int64_t where = 0;
-    if (MODE != kNormRope) {
-        where = token_row(a.p, a.c, t);
-        if (where < 0) {
-            if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
-            return;
-        }
-    }
-    auto normed = [&](float (&x)[8], const float (&w)[8]) {
-        float ss = 0.f;
+    const int64_t stride = ((int64_t)gridDim.x * kWarps) >> share_shift;
+    for (int64_t t = gw >> share_shift; t < a.T; t += stride) {
+        const T* q0 = static_cast<const T*>(a.q) + t * a.ld_q + sub * D;
+        const T* k0 = static_cast<const T*>(a.k) + t * a.ld_k + sub * D;
+        const T* v0 = static_cast<const T*>(a.v) + t * a.ld_v + sub * D;
+        Vec4<T> raw[kBatch][2];
+        auto load = [&](int g0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = 1.f / sqrtf(ss / (float)D + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
-        if (!turned) return;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // (every index a constant: x stays in registers)
-            const float p = a.interleaved ? x[2 * e] : x[e], q = a.interleaved ? x[2 * e + 1] : x[e + 4];
-            const float y = p * cs[e] - q * sn[e], z = q * cs[e] + p * sn[e];
-            if (a.interleaved) {
-                x[2 * e] = y;
-                x[2 * e + 1] = z;
-            } else {
-                x[e] = y;
-                x[e + 4] = z;
+            for (int u = 0; u < kBatch; ++u) {
+                const int g = g0 + (u << share_shift);
+                if (g >= groups) break;
+                if (MODE != kCacheWrite && g < nq) {
+                    if (on && g * RW + sub < a.H) {
+                        raw[u][0].load(q0 + g * (RW * D) + p0);
+                        raw[u][1].load(q0 + g * (RW * D) + p1);
+                    }
+                } else if (g < nq + nk) {
+                    if (on && (g - nq) * RW + sub < a.Hk) {
+                        raw[u][0].load(k0 + (g - nq) * (RW * D) + p0);
+                        raw[u][1].load(k0 + (g - nq) * (RW * D) + p1);
+                    }
+                } else if (MODE != kNormRope) {
+                    if (on && (g - nq - nk) * RW + sub < a.Hk) {
+                        raw[u][0].load(v0 + (g - nq - nk) * (RW * D) + 8 * l);
+                        raw[u][1].load(v0 + (g - nq - nk) * (RW * D) + 8 * l + 4);
+                    }
+                }
+            }
+        };
+        load(part);
+        float cs[4], sn[4];
+        if (MODE != kCacheWrite) {
+            float* cw = trig + warp * 2 * half;
+            const double pos = (double)a.pos[t] * 0.15915494309189533577;  // 1 / (2 pi)
+            __syncwarp();  // the last token's angles are read
+            for (int i = lane; i < half; i += 32) {
+                const double turns = pos * a.inv_freq[i];
+                sincospif(2.f * (float)(turns - rint(turns)), &cw[half + i], &cw[i]);
+            }
+            __syncwarp();
+            if (turned) {
+                const float4 x = *reinterpret_cast<const float4*>(cw + 4 * l);
+                const float4 y = *reinterpret_cast<const float4*>(cw + half + 4 * l);
+                cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
+                sn[0] = y.x; sn[1] = y.y; sn[2] = y.z; sn[3] = y.w;
             }
         }
-    };
-    for (int g0 = part; g0 < groups; g0 += kBatch << share_shift) {
-        if (g0 != part) load(g0);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int g = g0 + (u << share_shift);
-            if (g >= groups) break;
-            const bool is_q = g < nq, is_v = g >= nq + nk;
-            const int j = (is_q ? g : is_v ? g - nq - nk : g - nq) * RW + sub;
-            const bool live = on && j < (is_q ? a.H : a.Hk);
-            float x[8];
-            if (live) {
-                raw[u][0].get(x);
-                raw[u][1].get(x + 4);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            }
-            if (MODE != kCacheWrite && is_q) {
-                normed(x, wq);
-                if (live) put44(static_cast<T*>(a.q_out) + (t * a.H + j) * D, p0, p1, x);
+        int64_t where = 0;
+        if (MODE != kNormRope) {
+            where = token_row(a.p, a.c, t);
+            if (where < 0) {
+                if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
                 continue;
             }
-            if (MODE != kCacheWrite && !is_v) normed(x, wk);
-            if (MODE == kNormRope) {
-                if (live) put44(static_cast<T*>(a.k_out) + (t * a.Hk + j) * D, p0, p1, x);
-            } else {
-                put_cache<LPR>(a.c, is_v, where + ((int64_t)j << a.c.page_shift), l, is_v ? 8 * l : p0,
-                               is_v ? 8 * l + 4 : p1, live, x);
+            where += (int64_t)sub << a.c.page_shift;
+        }
+        T* const qo = static_cast<T*>(a.q_out) + t * a.H * D + sub * D;
+        T* const ko = static_cast<T*>(a.k_out) + t * a.Hk * D + sub * D;
+        auto normed = [&](float (&x)[8], const float (&w)[8]) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+            if (!turned) return;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float& p = x[INTER ? 2 * e : e];
+                float& q = x[INTER ? 2 * e + 1 : e + 4];
+                const float y = p * cs[e] - q * sn[e];
+                q = q * cs[e] + p * sn[e];
+                p = y;
+            }
+        };
+        for (int g0 = part; g0 < groups; g0 += kBatch << share_shift) {
+            if (g0 != part) load(g0);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int g = g0 + (u << share_shift);
+                if (g >= groups) break;
+                float x[8];
+                raw[u][0].get(x);
+                raw[u][1].get(x + 4);
+                if (!on) {  // (lanes past the row hold what was loaded before)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                }
+                if (MODE != kCacheWrite && g < nq) {
+                    normed(x, wq);
+                    if (on && g * RW + sub < a.H) put44(qo + g * (RW * D), p0, p1, x);
+                } else if (g < nq + nk) {
+                    if (MODE != kCacheWrite) normed(x, wk);
+                    const bool live = on && (g - nq) * RW + sub < a.Hk;
+                    if (MODE == kNormRope) {
+                        if (live) put44(ko + (g - nq) * (RW * D), p0, p1, x);
+                    } else {
+                        put_cache<LPR>(a.c, false, where + ((int64_t)((g - nq) * RW) << a.c.page_shift), l, p0, p1, live, x);
+                    }
+                } else if (MODE != kNormRope) {
+                    put_cache<LPR>(a.c, true, where + ((int64_t)((g - nq - nk) * RW) << a.c.page_shift), l, 8 * l, 8 * l + 4,
+                                   on && (g - nq - nk) * RW + sub < a.Hk, x);
+                }
             }
         }
     }
@@ -242,18 +270,30 @@ int share_of_token(int64_t T, int groups) {
     return s;
 }
 
+// CTAs for that many warps: at most eight to an SM, which then walk the tokens.
+unsigned grid_of(int64_t warps) {
+    const int64_t need = (warps + kWarps - 1) / kWarps, most = 8 * (int64_t)sm_count();
+    return (unsigned)(need < most ? need : most);
+}
+
 template <typename T, int LPR>
 cudaError_t launch_lpr(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
     constexpr int RW = 32 / LPR;
     const int nk = (a.Hk + RW - 1) / RW;
     const int groups = mode == kCacheWrite ? 2 * nk : (a.H + RW - 1) / RW + (mode == kNormRope ? nk : 2 * nk);
     const int share = share_of_token(a.T, groups);
-    const unsigned grid = (unsigned)(((a.T << share) + kWarps - 1) / kWarps);
+    const unsigned grid = grid_of(a.T << share);
     const size_t smem = mode == kCacheWrite ? 0 : sizeof(float) * kWarps * a.rotary;
     switch (mode) {
-        case kNormRope: rows_kernel<T, LPR, kNormRope><<<grid, kThreads, smem, s>>>(a, share); break;
-        case kNormRopeCache: rows_kernel<T, LPR, kNormRopeCache><<<grid, kThreads, smem, s>>>(a, share); break;
-        case kCacheWrite: rows_kernel<T, LPR, kCacheWrite><<<grid, kThreads, smem, s>>>(a, share); break;
+        case kNormRope:
+            if (a.interleaved) rows_kernel<T, LPR, kNormRope, true><<<grid, kThreads, smem, s>>>(a, share);
+            else rows_kernel<T, LPR, kNormRope, false><<<grid, kThreads, smem, s>>>(a, share);
+            break;
+        case kNormRopeCache:
+            if (a.interleaved) rows_kernel<T, LPR, kNormRopeCache, true><<<grid, kThreads, smem, s>>>(a, share);
+            else rows_kernel<T, LPR, kNormRopeCache, false><<<grid, kThreads, smem, s>>>(a, share);
+            break;
+        case kCacheWrite: rows_kernel<T, LPR, kCacheWrite, false><<<grid, kThreads, smem, s>>>(a, share); break;
     }
     return cudaGetLastError();
 }
