@@ -82,44 +82,49 @@ __device__ __forceinline__ float reciprocal(float s) {  // within an ulp, for no
     return fmaf(fmaf(-s, r, 1.f), r, r);
 }
 
+__device__ __forceinline__ float max_abs_nan(float m, float x) {  // max(m, |x|), NaN if either is
+    float y;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(y) : "f"(m), "f"(x));
+    return y;
+}
+
 // Stores one row's eight elements per lane in the cache; every lane of the
 // group takes part (the amax is the group's). A row with an element that is
 // not finite is stored as scale NaN: it reads back as NaN.
 template <int LPR>
-__device__ __forceinline__ void put_cache(const CacheView& c, bool is_v, int64_t row, int l, int p0, int p1, bool on,
+__device__ __forceinline__ void put_cache(int e4m3, uint8_t* row, float* scale_at, int l, int p0, int p1, bool on,
                                           float (&x)[8]) {
-    if (!c.e4m3) {
-        if (on) put44(static_cast<uint16_t*>(is_v ? c.v : c.k) + row * c.D, p0, p1, x);
+    if (!e4m3) {
+        if (on) put44(reinterpret_cast<uint16_t*>(row), p0, p1, x);
         return;
     }
-    uint32_t m = 0;  // bits of |x| order as the values do, with inf and NaN on top
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) m = max_abs_nan(m, x[i]);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = LPR / 2; o > 0; o >>= 1) m = max_abs_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float scale;
-    if (m - 0x0D800000u < 0x72000000u - 0x0D800000u) {  // 2^-100 <= amax < 2^101
-        scale = corrected(__uint_as_float(m), 448.f, 1.f / 448.f);
+    if (m >= 0x1p-100f && m <= 0x1p100f) {
+        scale = corrected(m, 448.f, 1.f / 448.f);
         const float r = reciprocal(scale);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = corrected(x[i], scale, r);
     } else {
-        const bool finite = m < 0x7F800000u;
-        scale = finite ? __uint_as_float(m) / 448.f : __uint_as_float(0x7FC00000u);
+        const bool finite = m <= FLT_MAX;
+        scale = finite ? m / 448.f : __uint_as_float(0x7FC00000u);
         const bool zero = !finite || scale == 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : __fdiv_rn(x[i], scale);
     }
     if (!on) return;
     const uint2 codes = to_e4m3x8(x);
-    uint8_t* p = static_cast<uint8_t*>(is_v ? c.v : c.k) + row * c.D;
     if (p1 == p0 + 4) {
-        *reinterpret_cast<uint2*>(p + p0) = codes;
+        *reinterpret_cast<uint2*>(row + p0) = codes;
     } else {
-        *reinterpret_cast<uint32_t*>(p + p0) = codes.x;
-        *reinterpret_cast<uint32_t*>(p + p1) = codes.y;
+        *reinterpret_cast<uint32_t*>(row + p0) = codes.x;
+        *reinterpret_cast<uint32_t*>(row + p1) = codes.y;
     }
-    if (l == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
+    if (l == 0) *scale_at = scale;
 }
 
 // Groups of 32 / LPR rows of a token: queries, keys, values. 1 << share_shift
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
         const T* q0 = static_cast<const T*>(a.q) + t * a.ld_q + sub * D;
         const T* k0 = static_cast<const T*>(a.k) + t * a.ld_k + sub * D;
         const T* v0 = static_cast<const T*>(a.v) + t * a.ld_v + sub * D;
-        Vec4<T> raw[kBatch][2];
+        Vec4<T> raw[kBatch][2] = {};  // (lanes past the row keep zeros)
         auto load = [&](int g0) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -209,6 +214,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
             }
             where += (int64_t)sub << a.c.page_shift;
         }
+        // this lane group's first cached row of the token; RW heads further is `step` rows on
+        const int row_bytes = a.c.e4m3 ? D : 2 * D, step = RW << a.c.page_shift;
+        uint8_t* const kd = static_cast<uint8_t*>(a.c.k) + where * row_bytes;
+        uint8_t* const vd = static_cast<uint8_t*>(a.c.v) + where * row_bytes;
+        float* const ks = a.c.k_scale + where;
+        float* const vs = a.c.v_scale + where;
         T* const qo = static_cast<T*>(a.q_out) + t * a.H * D + sub * D;
         T* const ko = static_cast<T*>(a.k_out) + t * a.Hk * D + sub * D;
         auto normed = [&](float (&x)[8], const float (&w)[8]) {
@@ -239,10 +250,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
                 float x[8];
                 raw[u][0].get(x);
                 raw[u][1].get(x + 4);
-                if (!on) {  // (lanes past the row hold what was loaded before)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-                }
                 if (MODE != kCacheWrite && g < nq) {
                     normed(x, wq);
                     if (on && g * RW + sub < a.H) put44(qo + g * (RW * D), p0, p1, x);
@@ -252,10 +259,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
                     if (MODE == kNormRope) {
                         if (live) put44(ko + (g - nq) * (RW * D), p0, p1, x);
                     } else {
-                        put_cache<LPR>(a.c, false, where + ((int64_t)((g - nq) * RW) << a.c.page_shift), l, p0, p1, live, x);
+                        const int at = (g - nq) * step;
+                        put_cache<LPR>(a.c.e4m3, kd + (int64_t)at * row_bytes, ks + at, l, p0, p1, live, x);
                     }
                 } else if (MODE != kNormRope) {
-                    put_cache<LPR>(a.c, true, where + ((int64_t)((g - nq - nk) * RW) << a.c.page_shift), l, 8 * l, 8 * l + 4,
+                    const int at = (g - nq - nk) * step;
+                    put_cache<LPR>(a.c.e4m3, vd + (int64_t)at * row_bytes, vs + at, l, 8 * l, 8 * l + 4,
                                    on && (g - nq - nk) * RW + sub < a.Hk, x);
                 }
             }
