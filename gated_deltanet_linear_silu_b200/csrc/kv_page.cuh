@@ -30,7 +30,7 @@ __device__ __forceinline__ int64_t token_row(const PageArgs& p, const CacheView&
 }
 
 // Eight e4m3 values from fp32, to nearest even, magnitudes above 448 to 448.
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8]) {
+__device__ __forceinline__ uint2 to_e4m3x8(const float* x) {
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -11,11 +11,11 @@
 // All of it is HBM-bound (each element read once, written once) if few
 // instructions go with a 16-byte piece. A warp takes one token (or a share of
 // its heads, where tokens are few) and walks its heads, 32 / LPR rows at a time,
-// LPR lanes of eight elements to a row: the norm and amax are shuffles within
-// the lane group, and the token's place in the cache, its angles and the
-// weights are looked up once for all its heads. Where pairs are the two halves
-// of the rotated part, a lane of that part takes four elements of either half,
-// so that a pair stays in one lane and the rotation exchanges nothing.
+// LPR lanes of sixteen elements to a row: the norm and amax are shuffles within
+// the lane group, and the token's place in the cache and its angles are looked
+// up once for all its heads. Where pairs are the two halves of the rotated part,
+// a lane of that part takes eight elements of either half, so that a pair stays
+// in one lane and the rotation exchanges nothing.
 //
 // The angle's turns, pos * inv_freq / (2 pi), are taken in fp64 and reduced to
 // [-1/2, 1/2] there: in fp32 a position of 2^18 would lose 2^-6 of a radian.
@@ -27,45 +27,45 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBatch = 4;  // row groups of a warp in flight
+constexpr int kBatch = 2;  // row groups of a warp in flight
 
-// Four consecutive elements, as loaded.
-template <typename T> struct Vec4;
-template <> struct Vec4<uint16_t> {
-    uint2 u;
-    __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint2*>(p)); }
+// Eight consecutive elements, as loaded.
+template <typename T> struct Vec8;
+template <> struct Vec8<uint16_t> {
+    uint4 u;
+    __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void get(float* x) const {
-        x[0] = __uint_as_float(u.x << 16);
-        x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(u.y << 16);
-        x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
     }
 };
-template <> struct Vec4<float> {
-    float4 f;
-    __device__ __forceinline__ void load(const float* p) { f = __ldcs(reinterpret_cast<const float4*>(p)); }
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+    }
     __device__ __forceinline__ void get(float* x) const {
-        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
 };
-__device__ __forceinline__ uint2 bf16x4(const float* x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void put8(uint16_t* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void put4(uint16_t* p, const float* x) { *reinterpret_cast<uint2*>(p) = bf16x4(x); }
-__device__ __forceinline__ void put4(float* p, const float* x) {
+__device__ __forceinline__ void put8(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-// Eight elements in two runs of four at p0 and p1; one store where they meet.
-template <typename T>
-__device__ __forceinline__ void put44(T* row, int p0, int p1, const float (&x)[8]) {
-    if (sizeof(T) == 2 && p1 == p0 + 4) {
-        const uint2 a = bf16x4(x), b = bf16x4(x + 4);
-        *reinterpret_cast<uint4*>(row + p0) = make_uint4(a.x, a.y, b.x, b.y);
-    } else {
-        put4(row + p0, x);
-        put4(row + p1, x + 4);
-    }
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
 // x / s rounded once, given r close to 1 / s (Markstein's correction: the
@@ -88,19 +88,23 @@ __device__ __forceinline__ float max_abs_nan(float m, float x) {  // max(m, |x|)
     return y;
 }
 
-// Stores one row's eight elements per lane in the cache; every lane of the
-// group takes part (the amax is the group's). A row with an element that is
-// not finite is stored as scale NaN: it reads back as NaN.
+// Stores one row's sixteen elements per lane in the cache, eight at p0 and eight
+// at p1; every lane of the group takes part (the amax is the group's). A row
+// with an element that is not finite is stored as scale NaN: it reads back as
+// NaN.
 template <int LPR>
 __device__ __forceinline__ void put_cache(int e4m3, uint8_t* row, float* scale_at, int l, int p0, int p1, bool on,
-                                          float (&x)[8]) {
+                                          float (&x)[16]) {
     if (!e4m3) {
-        if (on) put44(reinterpret_cast<uint16_t*>(row), p0, p1, x);
+        if (on) {
+            put8(reinterpret_cast<uint16_t*>(row) + p0, x);
+            put8(reinterpret_cast<uint16_t*>(row) + p1, x + 8);
+        }
         return;
     }
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_abs_nan(m, x[i]);
+    for (int i = 0; i < 16; ++i) m = max_abs_nan(m, x[i]);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) m = max_abs_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float scale;
@@ -108,62 +112,47 @@ __device__ __forceinline__ void put_cache(int e4m3, uint8_t* row, float* scale_a
         scale = corrected(m, 448.f, 1.f / 448.f);
         const float r = reciprocal(scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = corrected(x[i], scale, r);
+        for (int i = 0; i < 16; ++i) x[i] = corrected(x[i], scale, r);
     } else {
         const bool finite = m <= FLT_MAX;
         scale = finite ? m / 448.f : __uint_as_float(0x7FC00000u);
         const bool zero = !finite || scale == 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : __fdiv_rn(x[i], scale);
+        for (int i = 0; i < 16; ++i) x[i] = zero ? 0.f : __fdiv_rn(x[i], scale);
     }
     if (!on) return;
-    const uint2 codes = to_e4m3x8(x);
-    if (p1 == p0 + 4) {
-        *reinterpret_cast<uint2*>(row + p0) = codes;
-    } else {
-        *reinterpret_cast<uint32_t*>(row + p0) = codes.x;
-        *reinterpret_cast<uint32_t*>(row + p1) = codes.y;
-    }
+    *reinterpret_cast<uint2*>(row + p0) = to_e4m3x8(x);
+    *reinterpret_cast<uint2*>(row + p1) = to_e4m3x8(x + 8);
     if (l == 0) *scale_at = scale;
 }
 
 // Groups of 32 / LPR rows of a token: queries, keys, values. 1 << share_shift
 // warps take a token's groups in turn; INTER: pairs are neighbours.
 template <typename T, int LPR, int MODE, bool INTER>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(RowsArgs a, int share_shift) {
-    extern __shared__ float trig[];  // per warp: cos [half], sin [half]
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (MODE == kCacheWrite ? 4 : 3) : 2)
+rows_kernel(RowsArgs a, int share_shift) {
+    extern __shared__ __align__(16) float trig[];  // per warp: cos [half], sin [half]
     constexpr int RW = 32 / LPR;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, sub = lane / LPR;
     const int D = a.D, half = a.rotary >> 1;
-    const bool on = 8 * l < D;
+    const bool on = 16 * l < D;
     const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
     const int part = (int)(gw & ((1 << share_shift) - 1));
     const int nq = MODE == kCacheWrite ? 0 : (a.H + RW - 1) / RW, nk = (a.Hk + RW - 1) / RW;
     const int groups = nq + (MODE == kNormRope ? nk : 2 * nk);
     // this lane's elements of a normed row
-    const bool turned = MODE != kCacheWrite && 8 * l < a.rotary;
+    const bool turned = MODE != kCacheWrite && 16 * l < a.rotary;
     const bool split = turned && !INTER;
-    const int p0 = split ? 4 * l : 8 * l, p1 = split ? half + 4 * l : 8 * l + 4;
+    const int p0 = split ? 8 * l : 16 * l, p1 = split ? half + 8 * l : 16 * l + 8;
     const float inv_d = 1.f / (float)D;
-    float wq[8], wk[8];
-    if (MODE != kCacheWrite) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const int p = e ? p1 : p0;
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 x = on ? *reinterpret_cast<const float4*>(a.q_w + p) : z;
-            const float4 y = on ? *reinterpret_cast<const float4*>(a.k_w + p) : z;
-            wq[e] = x.x; wq[e + 1] = x.y; wq[e + 2] = x.z; wq[e + 3] = x.w;
-            wk[e] = y.x; wk[e + 1] = y.y; wk[e + 2] = y.z; wk[e + 3] = y.w;
-        }
-    }
+    float* const cw = trig + warp * 2 * half;
     const int64_t stride = ((int64_t)gridDim.x * kWarps) >> share_shift;
     for (int64_t t = gw >> share_shift; t < a.T; t += stride) {
         const T* q0 = static_cast<const T*>(a.q) + t * a.ld_q + sub * D;
         const T* k0 = static_cast<const T*>(a.k) + t * a.ld_k + sub * D;
         const T* v0 = static_cast<const T*>(a.v) + t * a.ld_v + sub * D;
-        Vec4<T> raw[kBatch][2] = {};  // (lanes past the row keep zeros)
+        Vec8<T> raw[kBatch][2] = {};  // (lanes past the row keep zeros)
         auto load = [&](int g0) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -181,16 +170,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
                     }
                 } else if (MODE != kNormRope) {
                     if (on && (g - nq - nk) * RW + sub < a.Hk) {
-                        raw[u][0].load(v0 + (g - nq - nk) * (RW * D) + 8 * l);
-                        raw[u][1].load(v0 + (g - nq - nk) * (RW * D) + 8 * l + 4);
+                        raw[u][0].load(v0 + (g - nq - nk) * (RW * D) + 16 * l);
+                        raw[u][1].load(v0 + (g - nq - nk) * (RW * D) + 16 * l + 8);
                     }
                 }
             }
         };
         load(part);
-        float cs[4], sn[4];
         if (MODE != kCacheWrite) {
-            float* cw = trig + warp * 2 * half;
             const double pos = (double)a.pos[t] * 0.15915494309189533577;  // 1 / (2 pi)
             __syncwarp();  // the last token's angles are read
             for (int i = lane; i < half; i += 32) {
@@ -198,12 +185,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
                 sincospif(2.f * (float)(turns - rint(turns)), &cw[half + i], &cw[i]);
             }
             __syncwarp();
-            if (turned) {
-                const float4 x = *reinterpret_cast<const float4*>(cw + 4 * l);
-                const float4 y = *reinterpret_cast<const float4*>(cw + half + 4 * l);
-                cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
-                sn[0] = y.x; sn[1] = y.y; sn[2] = y.z; sn[3] = y.w;
-            }
         }
         int64_t where = 0;
         if (MODE != kNormRope) {
@@ -222,23 +203,38 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
         float* const vs = a.c.v_scale + where;
         T* const qo = static_cast<T*>(a.q_out) + t * a.H * D + sub * D;
         T* const ko = static_cast<T*>(a.k_out) + t * a.Hk * D + sub * D;
-        auto normed = [&](float (&x)[8], const float (&w)[8]) {
+        auto normed = [&](float (&x)[16], const float* w) {
             float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+            if (on) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 y = __ldg(reinterpret_cast<const float4*>(w + (e < 8 ? p0 + e : p1 + e - 8)));
+                    x[e] = x[e] * inv * y.x;
+                    x[e + 1] = x[e + 1] * inv * y.y;
+                    x[e + 2] = x[e + 2] * inv * y.z;
+                    x[e + 3] = x[e + 3] * inv * y.w;
+                }
+            }
             if (!turned) return;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float& p = x[INTER ? 2 * e : e];
-                float& q = x[INTER ? 2 * e + 1 : e + 4];
-                const float y = p * cs[e] - q * sn[e];
-                q = q * cs[e] + p * sn[e];
-                p = y;
+            for (int e0 = 0; e0 < 8; e0 += 4) {
+                const float4 c4 = *reinterpret_cast<const float4*>(cw + 8 * l + e0);
+                const float4 s4 = *reinterpret_cast<const float4*>(cw + half + 8 * l + e0);
+                const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = e0 + i;
+                    float& p = x[INTER ? 2 * e : e];
+                    float& q = x[INTER ? 2 * e + 1 : e + 8];
+                    const float y = p * cs[i] - q * sn[i];
+                    q = q * cs[i] + p * sn[i];
+                    p = y;
+                }
             }
         };
         for (int g0 = part; g0 < groups; g0 += kBatch << share_shift) {
@@ -247,24 +243,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rows_kernel(
             for (int u = 0; u < kBatch; ++u) {
                 const int g = g0 + (u << share_shift);
                 if (g >= groups) break;
-                float x[8];
+                float x[16];
                 raw[u][0].get(x);
-                raw[u][1].get(x + 4);
+                raw[u][1].get(x + 8);
                 if (MODE != kCacheWrite && g < nq) {
-                    normed(x, wq);
-                    if (on && g * RW + sub < a.H) put44(qo + g * (RW * D), p0, p1, x);
+                    normed(x, a.q_w);
+                    if (on && g * RW + sub < a.H) {
+                        put8(qo + g * (RW * D) + p0, x);
+                        put8(qo + g * (RW * D) + p1, x + 8);
+                    }
                 } else if (g < nq + nk) {
-                    if (MODE != kCacheWrite) normed(x, wk);
+                    if (MODE != kCacheWrite) normed(x, a.k_w);
                     const bool live = on && (g - nq) * RW + sub < a.Hk;
                     if (MODE == kNormRope) {
-                        if (live) put44(ko + (g - nq) * (RW * D), p0, p1, x);
+                        if (live) {
+                            put8(ko + (g - nq) * (RW * D) + p0, x);
+                            put8(ko + (g - nq) * (RW * D) + p1, x + 8);
+                        }
                     } else {
                         const int at = (g - nq) * step;
                         put_cache<LPR>(a.c.e4m3, kd + (int64_t)at * row_bytes, ks + at, l, p0, p1, live, x);
                     }
                 } else if (MODE != kNormRope) {
                     const int at = (g - nq - nk) * step;
-                    put_cache<LPR>(a.c.e4m3, vd + (int64_t)at * row_bytes, vs + at, l, 8 * l, 8 * l + 4,
+                    put_cache<LPR>(a.c.e4m3, vd + (int64_t)at * row_bytes, vs + at, l, 16 * l, 16 * l + 8,
                                    on && (g - nq - nk) * RW + sub < a.Hk, x);
                 }
             }
@@ -309,11 +311,10 @@ cudaError_t launch_lpr(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_type(const RowsArgs& a, RowsMode mode, cudaStream_t s) {
-    if (a.D <= 16) return launch_lpr<T, 2>(a, mode, s);
-    if (a.D <= 32) return launch_lpr<T, 4>(a, mode, s);
-    if (a.D <= 64) return launch_lpr<T, 8>(a, mode, s);
-    if (a.D <= 128) return launch_lpr<T, 16>(a, mode, s);
-    return launch_lpr<T, 32>(a, mode, s);
+    if (a.D <= 32) return launch_lpr<T, 2>(a, mode, s);
+    if (a.D <= 64) return launch_lpr<T, 4>(a, mode, s);
+    if (a.D <= 128) return launch_lpr<T, 8>(a, mode, s);
+    return launch_lpr<T, 16>(a, mode, s);
 }
 
 // ---- reading back, the same walk: key rows, then value rows of a token.
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a, int share_sh
                     f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
                 }
             }
-            put44(dst, 8 * l, 8 * l + 4, f);
+            put8(dst + 8 * l, f);
         }
     }
 }
