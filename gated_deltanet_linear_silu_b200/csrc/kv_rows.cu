@@ -141,17 +141,19 @@ rows_kernel(RowsArgs a, int share_shift) {
     const int part = (int)(gw & ((1 << share_shift) - 1));
     const int nq = MODE == kCacheWrite ? 0 : (a.H + RW - 1) / RW, nk = (a.Hk + RW - 1) / RW;
     const int groups = nq + (MODE == kNormRope ? nk : 2 * nk);
-    // this lane's elements of a normed row
-    const bool turned = MODE != kCacheWrite && 16 * l < a.rotary;
-    const bool split = turned && !INTER;
-    const int p0 = split ? 8 * l : 16 * l, p1 = split ? half + 8 * l : 16 * l + 8;
+    // This lane's elements: eight of either half of the row, or, where pairs are the
+    // halves of a rotated part, of either half of that part or of the rest.
+    const bool turned = MODE != kCacheWrite && !INTER && 16 * l < a.rotary;
+    const int v0 = 8 * l, v1 = (D >> 1) + 8 * l;
+    const int p0 = MODE == kCacheWrite || INTER || turned ? v0 : half + v0;
+    const int p1 = MODE == kCacheWrite || INTER ? v1 : turned ? half + v0 : v1;
     const float inv_d = 1.f / (float)D;
     float* const cw = trig + warp * 2 * half;
     const int64_t stride = ((int64_t)gridDim.x * kWarps) >> share_shift;
     for (int64_t t = gw >> share_shift; t < a.T; t += stride) {
         const T* q0 = static_cast<const T*>(a.q) + t * a.ld_q + sub * D;
         const T* k0 = static_cast<const T*>(a.k) + t * a.ld_k + sub * D;
-        const T* v0 = static_cast<const T*>(a.v) + t * a.ld_v + sub * D;
+        const T* vt = static_cast<const T*>(a.v) + t * a.ld_v + sub * D;
         Vec8<T> raw[kBatch][2] = {};  // (lanes past the row keep zeros)
         auto load = [&](int g0) {
 #pragma unroll
@@ -170,8 +172,8 @@ rows_kernel(RowsArgs a, int share_shift) {
                     }
                 } else if (MODE != kNormRope) {
                     if (on && (g - nq - nk) * RW + sub < a.Hk) {
-                        raw[u][0].load(v0 + (g - nq - nk) * (RW * D) + 16 * l);
-                        raw[u][1].load(v0 + (g - nq - nk) * (RW * D) + 16 * l + 8);
+                        raw[u][0].load(vt + (g - nq - nk) * (RW * D) + v0);
+                        raw[u][1].load(vt + (g - nq - nk) * (RW * D) + v1);
                     }
                 }
             }
@@ -203,37 +205,52 @@ rows_kernel(RowsArgs a, int share_shift) {
         float* const vs = a.c.v_scale + where;
         T* const qo = static_cast<T*>(a.q_out) + t * a.H * D + sub * D;
         T* const ko = static_cast<T*>(a.k_out) + t * a.Hk * D + sub * D;
-        auto normed = [&](float (&x)[16], const float* w) {
+        float w[16];            // weights of the rows at hand
+        const float* held = nullptr;
+        auto normed = [&](float (&x)[16], const float* weights) {
+            if (held != weights) {  // (uniform: queries come first, then keys)
+                held = weights;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 y = on ? __ldg(reinterpret_cast<const float4*>(weights + (e < 8 ? p0 + e : p1 + e - 8)))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[e] = y.x; w[e + 1] = y.y; w[e + 2] = y.z; w[e + 3] = y.w;
+                }
+            }
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
-            if (on) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 y = __ldg(reinterpret_cast<const float4*>(w + (e < 8 ? p0 + e : p1 + e - 8)));
-                    x[e] = x[e] * inv * y.x;
-                    x[e + 1] = x[e + 1] * inv * y.y;
-                    x[e + 2] = x[e + 2] * inv * y.z;
-                    x[e + 3] = x[e + 3] * inv * y.w;
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
+            auto turn = [](float& p, float& q, float c, float s) {
+                const float y = p * c - q * s;
+                q = q * c + p * s;
+                p = y;
+            };
+            if (INTER) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = h ? p1 : p0;
+                    if (at >= a.rotary) continue;
+                    const float4 c4 = *reinterpret_cast<const float4*>(cw + (at >> 1));
+                    const float4 s4 = *reinterpret_cast<const float4*>(cw + half + (at >> 1));
+                    turn(x[8 * h], x[8 * h + 1], c4.x, s4.x);
+                    turn(x[8 * h + 2], x[8 * h + 3], c4.y, s4.y);
+                    turn(x[8 * h + 4], x[8 * h + 5], c4.z, s4.z);
+                    turn(x[8 * h + 6], x[8 * h + 7], c4.w, s4.w);
                 }
-            }
-            if (!turned) return;
+            } else if (turned) {
 #pragma unroll
-            for (int e0 = 0; e0 < 8; e0 += 4) {
-                const float4 c4 = *reinterpret_cast<const float4*>(cw + 8 * l + e0);
-                const float4 s4 = *reinterpret_cast<const float4*>(cw + half + 8 * l + e0);
-                const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = e0 + i;
-                    float& p = x[INTER ? 2 * e : e];
-                    float& q = x[INTER ? 2 * e + 1 : e + 8];
-                    const float y = p * cs[i] - q * sn[i];
-                    q = q * cs[i] + p * sn[i];
-                    p = y;
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(cw + p0 + e);
+                    const float4 s4 = *reinterpret_cast<const float4*>(cw + half + p0 + e);
+                    turn(x[e], x[e + 8], c4.x, s4.x);
+                    turn(x[e + 1], x[e + 9], c4.y, s4.y);
+                    turn(x[e + 2], x[e + 10], c4.z, s4.z);
+                    turn(x[e + 3], x[e + 11], c4.w, s4.w);
                 }
             }
         };
@@ -266,7 +283,7 @@ rows_kernel(RowsArgs a, int share_shift) {
                     }
                 } else if (MODE != kNormRope) {
                     const int at = (g - nq - nk) * step;
-                    put_cache<LPR>(a.c.e4m3, vd + (int64_t)at * row_bytes, vs + at, l, 16 * l, 16 * l + 8,
+                    put_cache<LPR>(a.c.e4m3, vd + (int64_t)at * row_bytes, vs + at, l, v0, v1,
                                    on && (g - nq - nk) * RW + sub < a.Hk, x);
                 }
             }
