@@ -16,9 +16,10 @@ e4m3 rows           scale: the largest element's error / 448 and a division (e).
 attention           scores: D products and additions, off by D e sum|q||k| scale
                     each way, 2 more scalings; exp2 2 ulp: s = (D + 8) e size + 8 e.
                     A numerator is off by 2 s in total (its own and the total's)
-                    and by u(bf16) from its rounding; the sums over the row by
-                    at most L e (L <= 20000: under 2^-9 in the worst order; the
-                    kernel's are partial sums of 16 and less). Output u(bf16).
+                    and by u(bf16) from its rounding (f16, where the cache is e4m3, is
+                    finer); the sums over a row by e for each addition in a chain: no
+                    chain is longer than a CTA's stretch, under 2^15 tokens here: 2^-9.
+                    Output u(bf16).
 """
 import math
 
@@ -41,6 +42,13 @@ def _cuda():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     torch.cuda.set_device(DEV)
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    """No kernel of a test may have skipped work or given up a wait unnoticed."""
+    yield
+    gdn.check_device_status(DEV)
 
 
 def half_step(t):
@@ -537,6 +545,35 @@ def test_tree_attention_long(held):
     for _ in range(3):  # the same bits at every call
         again, lse2 = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=3, mask=mask.to(DEV), return_lse=True)
         assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D,G,nodes", [(64, 8, 40), (128, 4, 7), (256, 4, 17), (128, 16, 20)])
+def test_tree_attention_long_with_many_rows(held, D, G, nodes):
+    """The same with more rows than one group of eight or sixteen: hundreds of
+    tiles to a CTA, several row tiles, one short sequence beside the long one."""
+    lens, counts = [120000, 700], [nodes, 3]
+    pool = Pool(lens, counts, 2, D, 64, held, fill=83)
+    q = rnd(84, sum(counts), 2 * G, D, dtype=BF).to(DEV)
+    mask = trees(counts, 10)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=nodes, mask=mask.to(DEV), return_lse=True)
+    # the reference on some rows: nodes 0 and the last, every head
+    k, v = (pool.rows(0, range(lens[0]), name) for name in ("k", "v"))
+    base = lens[0] - nodes
+    for i in (0, nodes - 1):
+        seen = torch.tensor([j < base or bool(int(mask[i]) >> (j - base) & 1) for j in range(lens[0])])
+        for h in (0, G - 1, 2 * G - 1):
+            s = (k[:, h // G] @ q[i, h].cpu().double()) * D ** -0.5
+            s[~seen] = -math.inf
+            z = torch.logsumexp(s, 0)
+            p = torch.exp(s - z)
+            size = (k[:, h // G].abs() @ q[i, h].cpu().double().abs()).max() * D ** -0.5
+            want, mass = p @ v[:, h // G], p @ v[:, h // G].abs()
+            e = float((D + 8) * E * size + 8 * E)
+            u = half_step(BF)
+            close(o[i, h], want, (u + 2 * e + 2.0 ** -9) * mass * (1 + u) + u * want.abs())
+            assert abs(float(lse[i, h]) - float(z)) <= e + 2.0 ** -9 + 8 * E * abs(float(z))
+    check_attention(pool, q, o, lse, mask, D ** -0.5, rows=[1])
 
 
 def test_tree_attention_bad_sequences():
