@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
     const int r = lane >> 2, c = lane & 3;
     const int G = a.H / a.c.Hk;
     pdl_launch_dependents();
+    pdl_wait_previous();
     const Share share = find_share<kRows, kTile, kThreads>(a);
 
     float* partials = partial_base(a);
@@ -535,6 +536,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int G = a.H / a.c.Hk;
     const int x = blockIdx.y * kWarps + (threadIdx.x >> 5);  // row of the (sequence, head)
     const int rt = x / ROWS, row = x % ROWS;
+    pdl_launch_dependents();
     const Seq seq = load_seq(a, n);  // (inputs of the call: not written by the kernel before)
     pdl_wait_previous();
     if (x >= seq.nodes * G) return;
@@ -642,8 +644,7 @@ cudaError_t launch_mma(const TreeArgs& a, cudaStream_t s) {
     using C = Config<D, E4M3, NT>;
     cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    tree_kernel<D, E4M3, NT><<<a.grid, kThreads, C::kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(tree_kernel<D, E4M3, NT>, dim3(a.grid), dim3(kThreads), C::kSmem, s, a);
 }
 
 template <int D, bool E4M3>
