@@ -213,7 +213,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     tc_fence_before();
     const Share share = find_share<kTcRows, TN, C::kThreads>(a);  // (synchronises the CTA)
     tc_fence_after();
-    const uint32_t tmem = B.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);  // (warp-uniform to the compiler)
     auto fail = [&]() {
         if (!*abort_flag) {
             *abort_flag = 1;
@@ -414,19 +414,22 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         if (!ok) fail();
     } else if (warp == kMmaWarp) {
         // ================================================================ products
-        // The whole warp walks the tiles alike and one elected lane issues: the
-        // descriptors are then warp-uniform values.
-        // Descriptors of the ring's first slot; a slot, a block or a k-step further
-        // is a constant added to the address field.
+        // The whole warp walks the tiles alike and one elected lane issues. The
+        // products' operands live in uniform registers; where the compiler cannot
+        // see that a value is the same in every lane it moves each of them there
+        // before each product, which costs more than the product. Hence the
+        // shuffles, and no way out of the loops but their counts: once a wait has
+        // run out the rest is walked without issuing anything.
         const uint64_t kd = sw128_desc(smem_u32(sm), 16, 1024), vd = sw128_desc(smem_u32(sm), C::kBlock, 1024);
         int ks = 0, vs = 1, kpar = 0, vpar = 0;  // slots of the next keys and values, their phases
         int sb = 0, pb = 0, ppar = 0;            // buffers of the next scores and probabilities
-        auto scores = [&]() -> bool {            // S of the next tile
-            if (!all_wait(&B.full[ks], kpar, abort_flag, wlim)) return false;
+        int og = 0;                              // accumulator of the next tile
+        auto scores = [&]() {                    // S of the next tile
+            ok = ok && all_wait(&B.full[ks], kpar, abort_flag, wlim);
             tc_fence_after();
             const uint64_t d0 = kd + (uint64_t)(ks * (C::kSlot >> 4));
             const uint32_t s0 = tmem + C::kColS + sb * TN;
-            if (elect_one()) {
+            if (elect_one() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_bf16_ta(s0, tmem + C::kColQ + 8 * kk, d0 + (((kk >> 2) * C::kBlock + 32 * (kk & 3)) >> 4), C::kIdescS,
@@ -437,27 +440,23 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             __syncwarp();
             if ((ks += 2) >= C::kSlots) ks = 0, kpar ^= 1;
             if (++sb == C::kBufs) sb = 0;
-            return true;
         };
-        int og = 0;  // accumulator of the next tile
-        for (int seg_no = 0; ok && have; ++seg_no) {
-            const int tiles = seg.tile1 - seg.tile0;
-            ok = all_wait(&B.qfull, seg_no & 1, abort_flag, wlim);
-            for (int y = 0; ok && y < tiles && y < C::kBufs; ++y) ok = scores();
-            if (ok && seg_no > 0) ok = all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim);
-            for (int y = 0; ok && y < tiles; ++y) {
-                if (!all_wait(&B.full[vs], vpar, abort_flag, wlim) || !all_wait(&B.pfull[pb], ppar, abort_flag, wlim)) {
-                    ok = false;
-                    break;
-                }
+        bool more_segs = __shfl_sync(0xffffffffu, (int)have, 0);
+        for (int seg_no = 0; more_segs; ++seg_no) {
+            const int tiles = __shfl_sync(0xffffffffu, seg.tile1 - seg.tile0, 0);
+            ok = ok && all_wait(&B.qfull, seg_no & 1, abort_flag, wlim);
+            for (int y = 0; y < C::kBufs && y < tiles; ++y) scores();
+            ok = ok && (seg_no == 0 || all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim));
+            for (int y = 0; y < tiles; ++y) {
+                ok = ok && all_wait(&B.full[vs], vpar, abort_flag, wlim) && all_wait(&B.pfull[pb], ppar, abort_flag, wlim);
                 tc_fence_after();
                 const uint64_t d0 = vd + (uint64_t)(vs * (C::kSlot >> 4));
-                const uint32_t p0 = tmem + C::kColS + pb * TN;
-                if (elect_one()) {
+                const uint32_t p0 = tmem + C::kColS + pb * TN, o0 = tmem + (C::kGroups ? og * D : 0);
+                const bool more = y >= (C::kGroups ? 2 : 1);  // the accumulator holds something
+                if (elect_one() && ok) {
 #pragma unroll
                     for (int kk = 0; kk < TN / 16; ++kk)
-                        mma_bf16_ta(tmem + (C::kGroups ? og * D : 0), p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO,
-                                    y >= (C::kGroups ? 2 : 1) || kk > 0);
+                        mma_bf16_ta(o0, p0 + 8 * kk, d0 + (2048 * kk >> 4), C::kIdescO, more || kk > 0);
                     mma_commit(&B.empty[vs]);
                     mma_commit(&B.odone[C::kGroups ? og : 0]);
                     if (y + 1 == tiles) mma_commit(&B.oend);
@@ -467,9 +466,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 if (++pb == C::kBufs) pb = 0, ppar ^= 1;
                 og ^= 1;
                 // the buffer of these probabilities takes the scores kBufs tiles on
-                if (y + C::kBufs < tiles) ok = scores();
+                if (y + C::kBufs < tiles) scores();
             }
-            have = ok && next_segment<kTcRows, TN>(a, share, seg);
+            more_segs = __shfl_sync(0xffffffffu, (int)(next_segment<kTcRows, TN>(a, share, seg)), 0);
         }
         if (!ok && lane == 0) fail();
         if (elect_one()) mma_commit(&B.drain);
