@@ -110,8 +110,10 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
     const int G = a.H / a.c.Hk;
-    pdl_launch_dependents();
+    // (in this order: the joining kernel reads the call's inputs before it waits, so
+    // it may start only when what wrote them is done)
     pdl_wait_previous();
+    pdl_launch_dependents();
     const Share share = find_share<kRows, kTile, kThreads>(a);
 
     float* partials = partial_base(a);
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int x = blockIdx.y * kWarps + (threadIdx.x >> 5);  // row of the (sequence, head)
     const int rt = x / ROWS, row = x % ROWS;
     pdl_launch_dependents();
-    const Seq seq = load_seq(a, n);  // (inputs of the call: not written by the kernel before)
+    const Seq seq = load_seq(a, n);  // (inputs of the call: complete before the kernel before let this one start)
     pdl_wait_previous();
     if (x >= seq.nodes * G) return;
     const UnitParts parts = *unit_parts(a, rt, n, hk);

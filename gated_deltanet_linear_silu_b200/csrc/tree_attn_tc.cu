@@ -181,6 +181,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (warp-uniform to the compiler)
     const int G = a.H / a.c.Hk;
     const uint64_t wlim = a.wait_ns;
+    pdl_wait_previous();  // (before its dependents, which read the call's inputs at once)
     pdl_launch_dependents();
 
     if (tid == 0) {
@@ -899,8 +900,7 @@ cudaError_t launch_tc(const TreeArgs& a, cudaStream_t s) {
     if (!E4M3 && (!make_map(&mk, a.c.k, a.c, run) || !make_map(&mv, a.c.v, a.c, run))) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    tree_tc_kernel<D, E4M3><<<a.grid, C::kThreads, C::kSmem, s>>>(a, mk, mv);
-    return cudaGetLastError();
+    return launch_pdl(tree_tc_kernel<D, E4M3>, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, a, mk, mv);
 }
 
 }  // namespace

@@ -720,6 +720,55 @@ def test_streams_graphs_and_workspaces():
         gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=6, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
 
 
+@pytest.mark.parametrize("rows", [4, 24])  # query rows: either kernel
+def test_inputs_written_just_before(rows):
+    """Lengths, queries and pages that the kernel before the call writes, on the
+    same stream and behind a long kernel: no part of a call may read them early."""
+    pool = Pool([4000, 300], [1, 1], 1, 64, 16, F8, fill=121)
+    q = torch.empty(2, rows, 64, dtype=BF, device=DEV)
+    qs = [rnd(122 + i, 2, rows, 64, dtype=BF).to(DEV) for i in range(4)]
+    lens = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([4000, 300], [17, 290], [3001, 1], [1, 299])]
+    table = pool.table.clone()
+    want = [gdn.tree_attention(x, pool.cache, table, l, pool.cu, max_nodes=1, return_lse=True) for x, l in zip(qs, lens)]
+    big = torch.randn(4096, 4096, device=DEV)
+    moving, pages = torch.empty_like(lens[0]), torch.empty_like(table)
+    for i in [0, 1, 2, 3] * 6:
+        big @ big
+        moving.copy_(lens[i])
+        pages.copy_(table)
+        q.copy_(qs[i])
+        o, lse = gdn.tree_attention(q, pool.cache, pages, moving, pool.cu, max_nodes=1, return_lse=True)
+        moving.zero_()  # and nothing reads them late
+        pages.fill_(-1)
+        q.zero_()
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+    # lengths straight from the call that accepts a draft
+    for i in range(8):
+        new = gdn.kv_cache_accept(pool.cache, table, lens[0], torch.tensor([0, 0, 0], dtype=torch.int32, device=DEV),
+                                  torch.empty((2, 0), dtype=torch.int32, device=DEV))
+        o = gdn.tree_attention(qs[0], pool.cache, table, new, pool.cu, max_nodes=1)
+        assert torch.equal(o, want[0][0])
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_waits_that_run_out_are_reported(D, held):
+    """With the limit at 0 every wait that is not over at its first probe gives up:
+    the kernel reports it, frees what it holds, and the next call is right."""
+    pool = Pool([3000, 100], [9, 2], 2, D, 32, held, fill=131)
+    q = rnd(132, 11, 8, D, dtype=BF).to(DEV)
+    gdn.set_wait_limit_ns(0)
+    try:
+        gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=9)
+        with pytest.raises(gdn.GDNError, match="TIMEOUT"):
+            gdn.check_device_status(DEV)
+    finally:
+        gdn.set_wait_limit_ns(-1)
+    torch.cuda.synchronize()
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=9, return_lse=True)
+    check_attention(pool, q, o, lse, None, D ** -0.5)
+
+
 @pytest.mark.parametrize("held", [F8, BF])
 def test_drafted_decoding_equals_plain_decoding(held):
     """Prompts, then rounds of drafting, verifying and accepting, captured steps
