@@ -62,8 +62,12 @@ struct Tc {
     static constexpr int kBlocks = D / 64;
     static constexpr int kSlot = kBlock * kBlocks;
     static constexpr int kSlots = D == 256 ? (E4M3 ? 4 : 6) : (E4M3 ? 8 : 12);  // (even: two to a tile)
-    // raw e4m3 tiles: TN rows of D bytes, then TN scales
-    static constexpr int kRaw = TN * D + TN * 4, kRawSlots = E4M3 ? (D == 256 ? 4 : 6) : 1;
+    // A tile's keys and values under one barrier: a wait and a hand-over fewer. Not
+    // where only two tiles fit the ring and the values, converted last, would hold
+    // up the scores.
+    static constexpr bool kOneFull = !(E4M3 && D == 256);
+    // raw e4m3 tiles: rows of D bytes of keys, then of values, then their scales
+    static constexpr int kRaw = 2 * (TN * D + TN * 4), kRawSlots = E4M3 ? (D == 256 ? 2 : 3) : 1;
     static constexpr int kOffRaw = kSlots * kSlot;
     static constexpr int kOffScale = kOffRaw + (E4M3 ? kRawSlots * kRaw : 0);  // [slot][k, v, log2 v][TN]
     static constexpr int kScaleBytes = E4M3 ? kScaleSlots * 3 * TN * 4 : 0;
@@ -83,9 +87,9 @@ struct Tc {
 };
 
 struct TcBars {
-    uint64_t full[12], empty[12];    // slots of the products (converter warps; bf16: loader, or one of them / commit)
-    uint64_t hand[12];               // bf16: slot left to the converters (loader)
-    uint64_t rfull[6], rempty[6];    // raw slots (bulk copies / converter warps)
+    uint64_t full[12], empty[12];    // slots of the products (converter warps, bf16: or as many by the loader / commit)
+    uint64_t hand[12];               // bf16: tile left to the converters (loader)
+    uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / converter warps)
     uint64_t cfull[kScaleSlots];     // a tile's scales (converter warps)
     uint64_t sfull[3], pfull[3];     // scores (commit), probabilities (4 or 8 warps)
     uint64_t odone[2];               // output product of a tile done, per accumulator (commit)
@@ -186,11 +190,11 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
 
     if (tid == 0) {
         for (int i = 0; i < 12; ++i) {
-            mbar_init(&B.full[i], E4M3 ? kConvWarps : 1);
+            mbar_init(&B.full[i], kConvWarps);
             mbar_init(&B.empty[i], 1);
             mbar_init(&B.hand[i], 1);
         }
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&B.rfull[i], 1);
             mbar_init(&B.rempty[i], kConvWarps);
         }
@@ -262,50 +266,54 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     id = 0;  // some rows of the pool: the sequence's output means nothing
                 }
                 const int row = ((id * a.c.Hk + seg.hk) << a.c.page_shift) + ((tile * TN + at * run) & (page - 1));
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (E4M3) {
-                        if (!all_wait(&B.rempty[rst], rpar, abort_flag, wlim)) { ok = false; break; }
-                        uint8_t* dst = sm + C::kOffRaw + rst * C::kRaw;
-                        if (lane == 0) mbar_arrive_expect_tx(&B.rfull[rst], (uint32_t)(n_runs * run * (D + 4)));
-                        last_full |= 1u << rst;
-                        last_par = (last_par & ~(1u << rst)) | (uint32_t)(rpar ^ 1) << rst;
-                        __syncwarp();
-                        if (lane < n_runs) {
-                            bulk_load(dst + lane * run * D, static_cast<const uint8_t*>(kv ? a.c.v : a.c.k) + (int64_t)row * D,
-                                      run * D, &B.rfull[rst]);
-                            bulk_load(dst + TN * D + lane * run * 4, (kv ? a.c.v_scale : a.c.k_scale) + row, run * 4,
-                                      &B.rfull[rst]);
-                        }
-                        __syncwarp();
-                        if (++rst == C::kRawSlots) rst = 0, rpar ^= 1;
-                    } else {
-                        if (!all_wait(&B.empty[st], par, abort_flag, wlim)) { ok = false; break; }
-                        if (by_hand(seg, tile)) {  // (the converters walk only these: a slot's phases are followed here)
-                            if (lane == 0) mbar_arrive(&B.hand[st]);
-                        } else {
-                            uint8_t* dst = sm + st * C::kSlot;
-                            last_full |= 1u << st;
-                            last_par = (last_par & ~(1u << st)) | (uint32_t)(par ^ 1) << st;
-                            if (run == TN) {
-                                if (elect_one()) {
-                                    mbar_arrive_expect_tx(&B.full[st], C::kSlot);
-                                    tma_load_3d(dst, kv ? &map_v : &map_k, &B.full[st], 0, row, 0);
-                                }
-                            } else {
-                                if (lane == 0) mbar_arrive_expect_tx(&B.full[st], C::kSlot);
-                                __syncwarp();
-                                if (lane < runs) {
-#pragma unroll
-                                    for (int b = 0; b < C::kBlocks; ++b)
-                                        tma_load_3d(dst + b * C::kBlock + lane * run * 128, kv ? &map_v : &map_k, &B.full[st],
-                                                    0, row, b);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        if (++st == C::kSlots) st = 0, par ^= 1;
+                if (E4M3) {
+                    if (!all_wait(&B.rempty[rst], rpar, abort_flag, wlim)) { ok = false; break; }
+                    uint8_t* dst = sm + C::kOffRaw + rst * C::kRaw;
+                    if (lane == 0) mbar_arrive_expect_tx(&B.rfull[rst], (uint32_t)(2 * n_runs * run * (D + 4)));
+                    last_full |= 1u << rst;
+                    last_par = (last_par & ~(1u << rst)) | (uint32_t)(rpar ^ 1) << rst;
+                    __syncwarp();
+                    if (lane < n_runs) {
+                        const int at_row = lane * run;
+                        bulk_load(dst + at_row * D, static_cast<const uint8_t*>(a.c.k) + (int64_t)row * D, run * D, &B.rfull[rst]);
+                        bulk_load(dst + (TN + at_row) * D, static_cast<const uint8_t*>(a.c.v) + (int64_t)row * D, run * D,
+                                  &B.rfull[rst]);
+                        bulk_load(dst + 2 * TN * D + at_row * 4, a.c.k_scale + row, run * 4, &B.rfull[rst]);
+                        bulk_load(dst + 2 * TN * D + (TN + at_row) * 4, a.c.v_scale + row, run * 4, &B.rfull[rst]);
                     }
+                    __syncwarp();
+                    if (++rst == C::kRawSlots) rst = 0, rpar ^= 1;
+                } else {
+                    if (!all_wait(&B.empty[st], par, abort_flag, wlim) || !all_wait(&B.empty[st + 1], par, abort_flag, wlim)) {
+                        ok = false;
+                        break;
+                    }
+                    if (by_hand(seg, tile)) {  // (the converters walk only these: the slots' phases are followed here)
+                        if (lane == 0) mbar_arrive(&B.hand[st]);
+                    } else {
+                        uint8_t* dst = sm + st * C::kSlot;
+                        last_full |= 1u << st;
+                        last_par = (last_par & ~(1u << st)) | (uint32_t)(par ^ 1) << st;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&B.full[st], 2 * C::kSlot);
+                            mbar_arrive(&B.full[st]);
+                            if (run == TN) {
+                                tma_load_3d(dst, &map_k, &B.full[st], 0, row, 0);
+                                tma_load_3d(dst + C::kSlot, &map_v, &B.full[st], 0, row, 0);
+                            }
+                        }
+                        __syncwarp();
+                        if (run < TN && lane < runs) {
+#pragma unroll
+                            for (int b = 0; b < C::kBlocks; ++b) {
+                                uint8_t* d = dst + b * C::kBlock + lane * run * 128;
+                                tma_load_3d(d, &map_k, &B.full[st], 0, row, b);
+                                tma_load_3d(d + C::kSlot, &map_v, &B.full[st], 0, row, b);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if ((st += 2) == C::kSlots) st = 0, par ^= 1;
                 }
             }
         }
@@ -318,42 +326,41 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     } else if (warp >= kConvWarp0) {
         // =================================================== conversion, last tiles
         const int pt = tid - 32 * kConvWarp0;
-        int x = 0;
-        uint32_t hand_par = 0;  // per slot: phase of its next hand-over
+        static_assert(E4M3 ? 32 * kConvWarps == 2 * TN : kConvWarps == 2, "a thread per scale, a warp for keys and one for values");
+        int i = 0;                               // tile number in this CTA
+        int rs = 0, rpar = 0, st = 0, par = 1;   // raw slot and slot of its keys, their phases
+        uint32_t hand_par = 0;                   // per slot: phase of its next hand-over
         auto publish = [&](uint64_t* bar) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
         for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
-            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
+            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++i) {
                 const int left = seg.seq.len - tile * TN;  // tokens that exist, from the tile's first
+                if (E4M3) {
+                    if (!all_wait(&B.rfull[rs], rpar, abort_flag, wlim)) { ok = false; break; }
+                    const uint8_t* raw = sm + C::kOffRaw + rs * C::kRaw;
+                    {
+                        const int tok = pt % TN;
+                        const float s = tok < left ? reinterpret_cast<const float*>(raw + 2 * TN * D)[pt] : 0.f;
+                        float* out = scales + (i % kScaleSlots) * 3 * TN;
+                        out[pt] = s;
+                        if (pt >= TN) out[TN + pt] = log2_scale(s);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&B.cfull[i % kScaleSlots]);
+                    }
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++x) {
-                    const int st = x % C::kSlots;
-                    uint8_t* slot = sm + st * C::kSlot;
-                    if (E4M3) {
-                        const int rs = x % C::kRawSlots;
-                        if (!all_wait(&B.rfull[rs], (x / C::kRawSlots) & 1, abort_flag, wlim)) { ok = false; break; }
-                        const uint8_t* raw = sm + C::kOffRaw + rs * C::kRaw;
-                        if (pt < TN) {
-                            const float s = reinterpret_cast<const float*>(raw + TN * D)[pt];
-                            float* out = scales + ((x >> 1) % kScaleSlots) * 3 * TN;
-                            out[kv * TN + pt] = pt < left ? s : 0.f;
-                            if (kv) out[2 * TN + pt] = log2_scale(pt < left ? s : 0.f);
-                        }
-                        if (kv) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&B.cfull[(x >> 1) % kScaleSlots]);
-                        }
-                        if (!all_wait(&B.empty[st], ((x / C::kSlots) & 1) ^ 1, abort_flag, wlim)) { ok = false; break; }
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!all_wait(&B.empty[st + kv], par, abort_flag, wlim)) { ok = false; break; }
+                        uint8_t* slot = sm + (st + kv) * C::kSlot;
                         // A lane takes 16-byte pieces of every second token: piece col of block
                         // y ^ h, h the token's parity. Eight lanes then read 64 bytes each of
                         // two rows, in different bank groups, and write two rows of two blocks
                         // whose swizzles fall into different bank groups as well.
                         const int col = lane & 3, h = (lane >> 2) & 1;
                         const int tok0 = 8 * (warp - kConvWarp0) + 2 * (lane >> 3) + h;
-                        const uint8_t* in = raw + tok0 * D + 16 * col;
+                        const uint8_t* in = raw + (kv * TN + tok0) * D + 16 * col;
                         uint8_t* out0 = slot + sw128_off(tok0, 2 * col);
                         uint8_t* out1 = slot + sw128_off(tok0, 2 * col + 1);
                         const bool whole = left >= TN;
@@ -378,10 +385,17 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                                                e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
                             }
                         }
-                        publish(&B.full[st]);
-                        if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
-                    } else {
-                        if (kv != warp - kConvWarp0 || !by_hand(seg, tile)) continue;  // a warp for keys, one for values
+                        if (!C::kOneFull) publish(&B.full[st + kv]);
+                    }
+                    if (!ok) break;
+                    if (C::kOneFull) publish(&B.full[st]);
+                    if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
+                    if (++rs == C::kRawSlots) rs = 0, rpar ^= 1;
+                    if ((st += 2) == C::kSlots) st = 0, par ^= 1;
+                } else {
+                    if (by_hand(seg, tile)) {
+                        const int kv = warp - kConvWarp0;  // a warp for keys, one for values
+                        uint8_t* slot = sm + (st + kv) * C::kSlot;
                         if (!all_wait(&B.hand[st], (hand_par >> st) & 1, abort_flag, wlim)) { ok = false; break; }
                         hand_par ^= 1u << st;
                         constexpr int kPer = D / 8;
@@ -409,6 +423,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         if (odd) *reinterpret_cast<volatile int*>(&B.odd) = 1;
                         publish(&B.full[st]);
                     }
+                    if ((st += 2) == C::kSlots) st = 0;
                 }
             }
         }
@@ -449,7 +464,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             for (int y = 0; y < C::kBufs && y < tiles; ++y) scores();
             ok = ok && (seg_no == 0 || all_wait(&B.ofree, (seg_no - 1) & 1, abort_flag, wlim));
             for (int y = 0; y < tiles; ++y) {
-                ok = ok && all_wait(&B.full[vs], vpar, abort_flag, wlim) && all_wait(&B.pfull[pb], ppar, abort_flag, wlim);
+                ok = ok && (C::kOneFull || all_wait(&B.full[vs], vpar, abort_flag, wlim)) &&
+                     all_wait(&B.pfull[pb], ppar, abort_flag, wlim);
                 tc_fence_after();
                 const uint64_t d0 = vd + (uint64_t)(vs * (C::kSlot >> 4));
                 const uint32_t p0 = tmem + C::kColS + pb * TN, o0 = tmem + (C::kGroups ? og * D : 0);
