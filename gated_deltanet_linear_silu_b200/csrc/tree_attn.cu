@@ -29,7 +29,6 @@
 // it, however the scales differ. R moves, and the sums are rescaled, only when
 // a weight would pass 2^8. Sums, maxima and outputs are fp32.
 #include <cfloat>
-#include <climits>
 
 #include "kv_page.cuh"
 #include "launch.h"
@@ -543,9 +542,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     pdl_wait_previous();
     if (x >= seq.nodes * G) return;
     const UnitParts parts = *unit_parts(a, rt, n, hk);
-    const int c0 = parts.first >> 1, count = parts.last - c0 + 1;
+    const int c0 = parts.first >> 1;
     // one CTA had the whole unit and wrote it (or the kernel before gave up: then these are anything)
-    if (count < 2 || parts.first < 0 || parts.last >= a.grid) return;
+    if (parts.first < 0 || parts.last <= c0 || parts.last >= a.grid) return;
+    const int count = parts.last - c0 + 1;
     const float* partials = partial_base(a);
     auto part = [&](int i) { return partials + (i == 0 ? parts.first : 2 * (c0 + i)) * slot_floats(D, a.slot_rows); };
     constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4s of a lane
@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     }
     if (a.lse && lane == 0) a.lse[t * a.H + head] = empty ? kNegInf : mt * kLn2 + logf(lt);
 }
-
 
 template <int D>
 int ctas_dim(int e4m3, int rows) {

@@ -47,7 +47,7 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kConvWarp0 = 10;
-constexpr int kScaleSlots = 8;  // (at least a tile's lead over the softmax, in tiles)
+constexpr int kScaleSlots = 8;  // tiles whose scales are kept
 constexpr uint64_t kDrainWaitNs = 1000000000ull;
 
 constexpr int TN = kTcTile;
@@ -77,6 +77,9 @@ struct Tc {
     // above half of the SM's shared memory, so that a CTA has its tensor memory to itself
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
+    // A tile's scales are written before its slots are waited for: the tile that
+    // had them before is one whose products are done, and its scales read.
+    static_assert(!E4M3 || kScaleSlots > kSlots / 2, "scales");
     // tensor memory: O (one or two), the queries, two or three buffers of S
     static constexpr int kBufs = kGroups ? 3 : 2;
     static constexpr int kColQ = kGroups ? 2 * D : D, kColS = kColQ + D / 2;

@@ -769,6 +769,24 @@ def test_waits_that_run_out_are_reported(D, held):
     check_attention(pool, q, o, lse, None, D ** -0.5)
 
 
+@pytest.mark.parametrize("word", [-1, 0x7FFFFFFF, -0x80000000, 0x7FFFFFFF - (1 << 32) * 0x80000000])
+def test_waits_that_run_out_leave_the_workspace_unread(word):
+    """Where the first kernel gave up before it noted where its partials are, the
+    words that were there mean nothing to the one that adds them up."""
+    pool = Pool([3000, 100], [9, 2], 2, 128, 32, F8, fill=133)
+    q = rnd(134, 11, 8, 128, dtype=BF).to(DEV)
+    size = gdn.tree_attention_workspace_size(pool.cache, 2, 8, 9)
+    ws = torch.full((size // 8,), word, dtype=torch.int64, device=DEV).view(torch.uint8)
+    gdn.set_wait_limit_ns(0)
+    try:
+        gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=9, workspace=ws)
+        with pytest.raises(gdn.GDNError, match="TIMEOUT"):
+            gdn.check_device_status(DEV)
+    finally:
+        gdn.set_wait_limit_ns(-1)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("held", [F8, BF])
 def test_drafted_decoding_equals_plain_decoding(held):
     """Prompts, then rounds of drafting, verifying and accepting, captured steps
