@@ -30,8 +30,11 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 bool act_ok(gdn_dtype_t t) { return t == GDN_F32 || t == GDN_BF16; }
 gdn_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
-// A head of a row: a multiple of 16 elements, up to 256 (32 lanes of eight).
+// A head of a row: a multiple of 16 elements, up to 256 (16 lanes of sixteen).
 bool row_dim_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
+
+// Heads of a token: the kernels count its elements, and the rows of a page, in 32 bits.
+constexpr int kMaxHeads = 1 << 16;
 
 // Token stride of a [T, heads, D] tensor whose rows are dense; 0: dense.
 gdn_status_t check_stride(int64_t& ld, int heads, int D, gdn_dtype_t dtype) {
@@ -44,7 +47,7 @@ gdn_status_t check_stride(int64_t& ld, int heads, int D, gdn_dtype_t dtype) {
 gdn_status_t check_cache(const gdn_kv_cache_t* c, gdn::CacheView* out) {
     if (!c || c->n_pages < 1 || c->Hk < 1) return GDN_ERR_INVALID_ARG;
     if (c->dtype != GDN_BF16 && c->dtype != GDN_E4M3) return GDN_ERR_INVALID_ARG;
-    if (!row_dim_ok(c->D)) return GDN_ERR_UNSUPPORTED;
+    if (!row_dim_ok(c->D) || c->Hk > kMaxHeads) return GDN_ERR_UNSUPPORTED;
     int shift = 0;
     while ((1 << shift) < c->page && shift < 20) ++shift;
     if (c->page < 16 || c->page > 1024 || (1 << shift) != c->page) return GDN_ERR_UNSUPPORTED;
@@ -68,7 +71,7 @@ gdn_status_t check_norm(int H, int Hk, int D, const float* q_w, const float* k_w
                         const double* inv_freq, int rotary, int interleaved) {
     if (H < 1 || Hk < 1 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
     if (interleaved != 0 && interleaved != 1) return GDN_ERR_INVALID_ARG;
-    if (!row_dim_ok(D)) return GDN_ERR_UNSUPPORTED;
+    if (!row_dim_ok(D) || H > kMaxHeads || Hk > kMaxHeads) return GDN_ERR_UNSUPPORTED;
     if (rotary < 0 || rotary > D) return GDN_ERR_INVALID_ARG;
     if (rotary % 16 != 0) return GDN_ERR_UNSUPPORTED;
     if (!aligned(q_w, 16) || !aligned(k_w, 16)) return GDN_ERR_INVALID_ARG;
@@ -179,7 +182,8 @@ gdn_status_t gdn_kv_accept(const gdn_kv_cache_t* cache, const int32_t* page_tabl
 }
 
 size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, int N, int H, int max_nodes) {
-    if (!cache || N < 0 || H <= 0 || cache->Hk <= 0 || max_nodes <= 0 ||
+    if (!cache || N < 0 || H <= 0 || cache->Hk <= 0 || cache->Hk > kMaxHeads || H % cache->Hk != 0 ||
+        H / cache->Hk > 64 || max_nodes <= 0 || max_nodes > gdn::kMaxNodes ||
         !(cache->D == 64 || cache->D == 128 || cache->D == 256))
         return 0;
     const size_t b = gdn::tree_workspace_bytes(N, H, cache->Hk, cache->D, max_nodes, cache->dtype == GDN_E4M3);

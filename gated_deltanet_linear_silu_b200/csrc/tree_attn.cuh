@@ -70,26 +70,11 @@ __device__ __forceinline__ bool zero_non_finite(uint32_t& x) {
     return x != y;
 }
 
-// bf16x2 of the two e4m3 codes in the high bytes of x's halves: sign to sign,
-// the other seven bits four places down, which leaves the value times 2^-120
-// (subnormals included); the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t x) {
-    const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-    uint32_t z;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0x7B807B80u));  // 2^120
-    return z;
-}
-
 // Asynchronous copies that write zeros where `on` is false (nothing is read).
 __device__ __forceinline__ void cp_async_zfill16(void* dst, const void* src, bool on) {
     const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
     const int n = on ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_zfill8(void* dst, const void* src, bool on) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int n = on ? 8 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_zfill4(void* dst, const void* src, bool on) {
     const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));

@@ -466,6 +466,7 @@ GDN_API gdn_status_t gdn_gated_rmsnorm(const void* y, const void* z, const float
  *   k, v               [n_pages, Hk, page, D]  dtype
  *   k_scale, v_scale   [n_pages, Hk, page]     fp32 (e4m3 only)
  *   page               tokens of a page: a power of two, 16 to 1024
+ *   Hk                 up to 65536
  *   D                  a multiple of 16, 16 to 256 (gdn_tree_attention: 64, 128, 256)
  *
  * The calls over a cache take, besides it,
@@ -480,7 +481,8 @@ GDN_API gdn_status_t gdn_gated_rmsnorm(const void* y, const void* z, const float
  * read into the cache, nor written in the outputs. A position whose page does
  * not exist (an id outside 0..n_pages-1, or past max_pages) and bounds that make
  * no sense set the device status word (GDN_ERR_INVALID_ARG); the tokens
- * concerned are skipped and everything else is done. Sequences may share pages
+ * concerned are skipped (gdn_tree_attention: see there) and everything else is
+ * done. Sequences may share pages
  * that a call only reads; a page that a call writes belongs to one sequence.
  */
 typedef struct {
@@ -511,7 +513,8 @@ typedef struct {
  *   inv_freq   [rotary/2]  fp64    radians per position (nullable: rotary 0)
  *   q_out      [T, H, D]   dtype   dense (may be q itself where q is dense)
  *   k_out      [T, Hk, D]  dtype   dense (may be k itself where k is dense)
- * Supported: D a multiple of 16, 16 to 256; rotary a multiple of 16, 0 to D.
+ * Supported: D a multiple of 16, 16 to 256; rotary a multiple of 16, 0 to D;
+ * up to 65536 heads. q, k, the outputs and the weights are 16-byte aligned.
  */
 GDN_API gdn_status_t gdn_qk_norm_rope(const void* q, const void* k, gdn_dtype_t dtype, int64_t T, int H, int Hk,
                                       int D, int64_t ld_q, int64_t ld_k, const float* q_w, const float* k_w,
@@ -575,8 +578,11 @@ GDN_API size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, in
  *   lse_i = log sum_j e^{scale q_i . k_j}.
  * A row that sees nothing is zero, with lse -infinity. What a row does not see
  * does not reach it, whatever it holds (infinities and NaN included). fp32
- * accumulation; the softmax's numerators are rounded to bf16 for the product
- * with the values. The result does not depend on what else runs, and for one
+ * accumulation; for the products the softmax's numerators are rounded to the
+ * type that the values take there: bf16 from a bf16 cache, f16 (11 bits) from an
+ * e4m3 one, whose scales are applied in fp32. A sequence with a position whose
+ * page does not exist is computed with other rows in its place: its output means
+ * nothing. The result does not depend on what else runs, and for one
  * set of arguments is the same bits at every call.
  *
  *   q          [T, H, D]  bf16   token stride ld_q elements (0: dense)
@@ -603,8 +609,8 @@ GDN_API const char* gdn_status_string(gdn_status_t status);
 /*
  * Diagnostic setting, process-wide: the limit in nanoseconds of each bounded
  * wait between the warp groups of the tensor-core prefill kernel and of the
- * wait for a state copy in the streaming whole-mixer decode step (the default
- * is 2 s; a negative value restores it). A wait that runs out records
+ * tensor-core tree attention, and of the wait for a state copy in the streaming
+ * whole-mixer decode step (the default is 2 s; a negative value restores it). A wait that runs out records
  * GDN_ERR_TIMEOUT in the device status word; the kernel then stops its work,
  * waits (again bounded) for the copies and tensor-core operations it has in
  * flight, frees its tensor memory and returns, leaving the context usable.

@@ -145,6 +145,21 @@ def test_tree_attention_refuses(L, kw, expect):
     assert attend(L, **kw) == expect
 
 
+def test_too_many_heads(L):
+    many = 1 << 17
+    assert norm_rope(L, H=many) == UNSUPPORTED and norm_rope(L, Hk=many) == UNSUPPORTED
+    assert rope_cache(L, H=many) == UNSUPPORTED
+    for call in (rope_cache, write, read, accept, attend):
+        assert call(L, cache=cache(Hk=many)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(H=5), dict(H=130), dict(max_nodes=65), dict(H=0), dict(max_nodes=0), dict(N=-1)])
+def test_workspace_size_of_unsupported_arguments(L, kw):
+    a = dict(N=1, H=4, max_nodes=2)
+    a.update(kw)
+    assert L.gdn_tree_attention_workspace_size(cache(), *a.values()) == 0
+
+
 def test_empty_calls_do_nothing(L):
     empty = dict(N=0, table=None, lens=None, cu=None)
     assert norm_rope(L, T=0, q=None, k=None) == OK
