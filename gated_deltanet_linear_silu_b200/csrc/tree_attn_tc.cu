@@ -55,9 +55,11 @@ constexpr int TN = kTcTile;
 template <int D, bool E4M3>
 struct Tc {
     static constexpr bool kGroups = D <= 128;  // even and odd tiles apart
-    // bf16 needs few converters, and 12 warps leave 168 registers to a thread
-    static constexpr int kConvWarps = E4M3 ? 4 : 2;
-    static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
+    // bf16 needs few converters, and 12 warps leave 168 registers to a thread;
+    // 13 to 16 warps leave 128
+    static constexpr int kConvWarps = E4M3 ? 4 : 2, kScaleWarps = E4M3 ? 2 : 0;
+    static constexpr int kScaleWarp0 = kConvWarp0 + kConvWarps;
+    static constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps);
     static constexpr int kBlock = TN * 128;  // 64 elements of every row, 128-byte swizzled
     static constexpr int kBlocks = D / 64;
     static constexpr int kSlot = kBlock * kBlocks;
@@ -77,9 +79,10 @@ struct Tc {
     // above half of the SM's shared memory, so that a CTA has its tensor memory to itself
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
-    // A tile's scales are written before its slots are waited for: the tile that
-    // had them before is one whose products are done, and its scales read.
-    static_assert(!E4M3 || kScaleSlots > kSlots / 2, "scales");
+    // A tile's scales are written as soon as its raw slot is full, which is when the
+    // tile before it in that slot is converted, and that when the tile before it in
+    // the products' slots is done: the scales of that one are read.
+    static_assert(!E4M3 || kScaleSlots >= kRawSlots + kSlots / 2, "scales");
     // tensor memory: O (one or two), the queries, two or three buffers of S
     static constexpr int kBufs = kGroups ? 3 : 2;
     static constexpr int kColQ = kGroups ? 2 * D : D, kColS = kColQ + D / 2;
@@ -92,8 +95,8 @@ struct Tc {
 struct TcBars {
     uint64_t full[12], empty[12];    // slots of the products (converter warps, bf16: or as many by the loader / commit)
     uint64_t hand[12];               // bf16: tile left to the converters (loader)
-    uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / converter warps)
-    uint64_t cfull[kScaleSlots];     // a tile's scales (converter warps)
+    uint64_t rfull[3], rempty[3];    // raw slots (bulk copies / converter and scale warps)
+    uint64_t cfull[kScaleSlots];     // a tile's scales (scale warps)
     uint64_t sfull[3], pfull[3];     // scores (commit), probabilities (4 or 8 warps)
     uint64_t odone[2];               // output product of a tile done, per accumulator (commit)
     uint64_t oend, ofree;            // of a segment: all of them done (commit), output read (8 warps)
@@ -199,9 +202,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&B.rfull[i], 1);
-            mbar_init(&B.rempty[i], kConvWarps);
+            mbar_init(&B.rempty[i], kConvWarps + C::kScaleWarps);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], kConvWarps);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&B.cfull[i], 2);
         for (int i = 0; i < 3; ++i) {
             mbar_init(&B.sfull[i], 1);
             mbar_init(&B.pfull[i], C::kGroups ? kSoftWarps / 2 : kSoftWarps);
@@ -326,11 +329,32 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             for (int x = 0; x < (E4M3 ? C::kRawSlots : C::kSlots); ++x)
                 if ((last_full >> x) & 1) mbar_wait(E4M3 ? &B.rfull[x] : &B.full[x], (last_par >> x) & 1, kDrainWaitNs);
         __syncwarp();
+    } else if (E4M3 && warp >= C::kScaleWarp0) {
+        // ================================================================= scales
+        // of keys (first warp) and of values, with their logarithms: two tokens a lane
+        const int kv = warp - C::kScaleWarp0;
+        int i = 0, rs = 0, rpar = 0, sl = 0;
+        for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg))
+            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++i) {
+                if (!all_wait(&B.rfull[rs], rpar, abort_flag, wlim)) { ok = false; break; }
+                const float2 raw = reinterpret_cast<const float2*>(sm + C::kOffRaw + rs * C::kRaw + 2 * TN * D)[kv * (TN / 2) + lane];
+                const int left = seg.seq.len - tile * TN - 2 * lane;
+                const float2 x = make_float2(left > 0 ? raw.x : 0.f, left > 1 ? raw.y : 0.f);
+                float2* out = reinterpret_cast<float2*>(scales + sl * 3 * TN) + kv * (TN / 2) + lane;
+                *out = x;
+                if (kv) out[TN / 2] = make_float2(log2_scale(x.x), log2_scale(x.y));
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&B.cfull[sl]);
+                    mbar_arrive(&B.rempty[rs]);
+                }
+                if (++rs == C::kRawSlots) rs = 0, rpar ^= 1;
+                if (++sl == kScaleSlots) sl = 0;
+            }
+        if (!ok) fail();
     } else if (warp >= kConvWarp0) {
         // =================================================== conversion, last tiles
-        const int pt = tid - 32 * kConvWarp0;
-        static_assert(E4M3 ? 32 * kConvWarps == 2 * TN : kConvWarps == 2, "a thread per scale, a warp for keys and one for values");
-        int i = 0;                               // tile number in this CTA
+        static_assert(E4M3 || kConvWarps == 2, "a warp for keys and one for values");
         int rs = 0, rpar = 0, st = 0, par = 1;   // raw slot and slot of its keys, their phases
         uint32_t hand_par = 0;                   // per slot: phase of its next hand-over
         auto publish = [&](uint64_t* bar) {
@@ -339,56 +363,49 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             if (lane == 0) mbar_arrive(bar);
         };
         for (; ok && have; have = ok && next_segment<kTcRows, TN>(a, share, seg)) {
-            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++i) {
+            for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile) {
                 const int left = seg.seq.len - tile * TN;  // tokens that exist, from the tile's first
                 if (E4M3) {
                     if (!all_wait(&B.rfull[rs], rpar, abort_flag, wlim)) { ok = false; break; }
                     const uint8_t* raw = sm + C::kOffRaw + rs * C::kRaw;
-                    {
-                        const int tok = pt % TN;
-                        const float s = tok < left ? reinterpret_cast<const float*>(raw + 2 * TN * D)[pt] : 0.f;
-                        float* out = scales + (i % kScaleSlots) * 3 * TN;
-                        out[pt] = s;
-                        if (pt >= TN) out[TN + pt] = log2_scale(s);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&B.cfull[i % kScaleSlots]);
-                    }
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!all_wait(&B.empty[st + kv], par, abort_flag, wlim)) { ok = false; break; }
-                        uint8_t* slot = sm + (st + kv) * C::kSlot;
-                        // A lane takes 16-byte pieces of every second token: piece col of block
-                        // y ^ h, h the token's parity. Eight lanes then read 64 bytes each of
-                        // two rows, in different bank groups, and write two rows of two blocks
-                        // whose swizzles fall into different bank groups as well.
-                        const int col = lane & 3, h = (lane >> 2) & 1;
-                        const int tok0 = 8 * (warp - kConvWarp0) + 2 * (lane >> 3) + h;
-                        const uint8_t* in = raw + (kv * TN + tok0) * D + 16 * col;
-                        uint8_t* out0 = slot + sw128_off(tok0, 2 * col);
-                        uint8_t* out1 = slot + sw128_off(tok0, 2 * col + 1);
-                        const bool whole = left >= TN;
-                        constexpr int kAhead = C::kBlocks > 1 ? 4 : 2;  // pieces: two tokens of one or two blocks
+                    // A lane takes 16-byte pieces of every second token: piece col of block
+                    // y ^ h, h the token's parity. Eight lanes then read 64 bytes each of
+                    // two rows, in different bank groups, and write two rows of two blocks
+                    // whose swizzles fall into different bank groups as well. A batch of
+                    // pieces is read before the one ahead of it is written.
+                    constexpr int kBatch = C::kBlocks > 1 ? 4 : 2;          // pieces: two tokens of one or two blocks
+                    constexpr int kSide = 2 * C::kBlocks / kBatch;          // batches of a tile's keys, or values
+                    const int col = lane & 3, h = (lane >> 2) & 1;
+                    const int tok0 = 8 * (warp - kConvWarp0) + 2 * (lane >> 3) + h;
+                    const uint8_t* in = raw + tok0 * D + 16 * col;
+                    uint8_t* const slot = sm + st * C::kSlot;
+                    const uint32_t at0 = sw128_off(tok0, 2 * col), at1 = sw128_off(tok0, 2 * col + 1);
+                    const bool whole = left >= TN;
+                    uint4 u[2][kBatch];
+                    auto block = [&](int b, int j) { return C::kBlocks > 1 ? (b % kSide * (kBatch / 2) + j / 2) ^ h : 0; };
+                    auto load = [&](int b) {
 #pragma unroll
-                        for (int y0 = 0; y0 < C::kBlocks; y0 += kAhead / 2) {
-                            uint4 u[kAhead];
-#pragma unroll
-                            for (int j = 0; j < kAhead; ++j) {
-                                const int block = C::kBlocks > 1 ? (y0 + j / 2) ^ h : 0;
-                                u[j] = *reinterpret_cast<const uint4*>(in + 32 * (j & 1) * D + 64 * block);
-                                if (!whole && tok0 + 32 * (j & 1) >= left) u[j] = make_uint4(0, 0, 0, 0);
-                            }
-#pragma unroll
-                            for (int j = 0; j < kAhead; ++j) {
-                                const int at = (C::kBlocks > 1 ? (y0 + j / 2) ^ h : 0) * C::kBlock + 32 * (j & 1) * 128;
-                                *reinterpret_cast<uint4*>(out0 + at) =
-                                    make_uint4(e4m3x2_to_f16x2(u[j].x), e4m3x2_to_f16x2(u[j].x >> 16),
-                                               e4m3x2_to_f16x2(u[j].y), e4m3x2_to_f16x2(u[j].y >> 16));
-                                *reinterpret_cast<uint4*>(out1 + at) =
-                                    make_uint4(e4m3x2_to_f16x2(u[j].z), e4m3x2_to_f16x2(u[j].z >> 16),
-                                               e4m3x2_to_f16x2(u[j].w), e4m3x2_to_f16x2(u[j].w >> 16));
-                            }
+                        for (int j = 0; j < kBatch; ++j) {
+                            u[b & 1][j] = *reinterpret_cast<const uint4*>(in + (b / kSide * TN + 32 * (j & 1)) * D + 64 * block(b, j));
+                            if (!whole && tok0 + 32 * (j & 1) >= left) u[b & 1][j] = make_uint4(0, 0, 0, 0);
                         }
-                        if (!C::kOneFull) publish(&B.full[st + kv]);
+                    };
+                    load(0);
+#pragma unroll
+                    for (int b = 0; b < 2 * kSide; ++b) {
+                        if (b + 1 < 2 * kSide) load(b + 1);
+                        if (b % kSide == 0) ok = ok && all_wait(&B.empty[st + b / kSide], par, abort_flag, wlim);
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) {
+                            uint8_t* out = slot + b / kSide * C::kSlot + block(b, j) * C::kBlock + 32 * (j & 1) * 128;
+                            const uint4 x = u[b & 1][j];
+                            *reinterpret_cast<uint4*>(out + at0) = make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16),
+                                                                             e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
+                            *reinterpret_cast<uint4*>(out + at1) = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16),
+                                                                             e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
+                        }
+                        if (!C::kOneFull && b % kSide == kSide - 1) publish(&B.full[st + b / kSide]);
                     }
                     if (!ok) break;
                     if (C::kOneFull) publish(&B.full[st]);
