@@ -600,13 +600,19 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                                 float2 s[16];
                                 tmem_ld32(s0 + c0, *reinterpret_cast<float(*)[32]>(&s[0]));
                                 tmem_wait_ld();
-                                if (E4M3) {
+                                if (E4M3) {  // scaled scores back to tensor memory; maxima are of the weights
 #pragma unroll
                                     for (int e = 0; e < 16; e += 2) {
                                         const float4 k4 = *reinterpret_cast<const float4*>(sc + c0 + 2 * e);
+                                        s[e] = mul2(s[e], mul2(mul_2, make_float2(k4.x, k4.y)));
+                                        s[e + 1] = mul2(s[e + 1], mul2(mul_2, make_float2(k4.z, k4.w)));
+                                    }
+                                    tmem_st32(s0 + c0, *reinterpret_cast<const float(*)[32]>(&s[0]));
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
                                         const float4 v4 = *reinterpret_cast<const float4*>(sc + 2 * TN + c0 + 2 * e);
-                                        s[e] = fma2(s[e], mul2(mul_2, make_float2(k4.x, k4.y)), make_float2(v4.x, v4.y));
-                                        s[e + 1] = fma2(s[e + 1], mul2(mul_2, make_float2(k4.z, k4.w)), make_float2(v4.z, v4.w));
+                                        s[e] = add2(s[e], make_float2(v4.x, v4.y));
+                                        s[e + 1] = add2(s[e + 1], make_float2(v4.z, v4.w));
                                     }
                                 }
                                 if (masked) {
@@ -650,6 +656,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             }
                             const float minus = ref == kNegInf ? 0.f : -ref;
                             const float2 minus_2 = make_float2(minus, minus);
+                            if (E4M3) tmem_wait_st();
 #pragma unroll
                             for (int c0 = 0; c0 < TN; c0 += 32) {
                                 float2 s[16];
@@ -659,23 +666,31 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                                 uint32_t p[16];
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    float2 k2 = mul_2;
-                                    if (E4M3) k2 = mul2(mul_2, *reinterpret_cast<const float2*>(sc + c0 + 2 * e));
-                                    float2 y = fma2(s[e], k2, minus_2);
+                                    float2 y = E4M3 ? add2(s[e], minus_2) : fma2(s[e], mul_2, minus_2);
                                     y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                                     if (masked) {  // nothing from a token that the row does not see
                                         if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
                                         if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
                                     }
                                     l2 = add2(l2, y);
-                                    if (E4M3) {
-                                        y = mul2(y, *reinterpret_cast<const float2*>(sc + TN + c0 + 2 * e));
-                                        if (masked) {  // (whatever its scale)
-                                            if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
-                                            if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
-                                        }
+                                    if (!E4M3) p[e] = pack_bf16(y.x, y.y);
+                                    else s[e] = y;
+                                }
+                                if (E4M3) {
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const float4 v4 = *reinterpret_cast<const float4*>(sc + TN + c0 + 2 * e);
+                                        s[e] = mul2(s[e], make_float2(v4.x, v4.y));
+                                        s[e + 1] = mul2(s[e + 1], make_float2(v4.z, v4.w));
                                     }
-                                    p[e] = E4M3 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        if (masked) {  // (whatever its scale)
+                                            if (!((bits >> (2 * e)) & 1)) s[e].x = 0.f;
+                                            if (!((bits >> (2 * e + 1)) & 1)) s[e].y = 0.f;
+                                        }
+                                        p[e] = pack_f16(s[e].x, s[e].y);
+                                    }
                                 }
                                 tmem_st16(s0 + c0 / 2, p);
                             }
@@ -711,10 +726,15 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         tmem_wait_ld();
                         const float2 mul_2 = make_float2(mul, mul);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 k2 = mul_2;
-                            if (E4M3) k2 = mul2(mul_2, *reinterpret_cast<const float2*>(sc + 2 * e));
+                        for (int e = 0; e < 16; e += 2) {
+                            float2 k2 = mul_2, k3 = mul_2;
+                            if (E4M3) {
+                                const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * e);
+                                k2 = mul2(mul_2, make_float2(k4.x, k4.y));
+                                k3 = mul2(mul_2, make_float2(k4.z, k4.w));
+                            }
                             s[e] = mul2(s[e], k2);
+                            s[e + 1] = mul2(s[e + 1], k3);
                         }
                         if (masked) {
 #pragma unroll
@@ -770,18 +790,27 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         uint32_t p[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float2 y = add2(s[e], minus_2);
-                            y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            l2 = add2(l2, y);
-                            if (E4M3) {
-                                y = mul2(y, *reinterpret_cast<const float2*>(sc + TN + 2 * e));
-                                if (masked) {  // nothing from a token that the row does not see, whatever its scale
-                                    if (!((bits >> (2 * e)) & 1)) y.x = 0.f;
-                                    if (!((bits >> (2 * e + 1)) & 1)) y.y = 0.f;
+                            s[e] = add2(s[e], minus_2);
+                            s[e] = make_float2(exp2_approx(s[e].x), exp2_approx(s[e].y));
+                            l2 = add2(l2, s[e]);
+                        }
+                        if (E4M3) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float4 v4 = *reinterpret_cast<const float4*>(sc + TN + 2 * e);
+                                s[e] = mul2(s[e], make_float2(v4.x, v4.y));
+                                s[e + 1] = mul2(s[e + 1], make_float2(v4.z, v4.w));
+                            }
+                            if (masked) {  // nothing from a token that the row does not see, whatever its scale
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    if (!((bits >> (2 * e)) & 1)) s[e].x = 0.f;
+                                    if (!((bits >> (2 * e + 1)) & 1)) s[e].y = 0.f;
                                 }
                             }
-                            p[e] = E4M3 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
                         }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = E4M3 ? pack_f16(s[e].x, s[e].y) : pack_bf16(s[e].x, s[e].y);
                         tmem_st16(s0 + half * HC / 2, p);
                         tmem_wait_st();
                     }
