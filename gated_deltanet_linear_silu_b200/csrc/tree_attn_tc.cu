@@ -595,7 +595,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             constexpr bool masked = decltype(masked_)::value;
                             const float2 mul_2 = make_float2(mul, mul);
                             float top = kNegInf, top_b = kNegInf;
-#pragma unroll
+                            // (e4m3: rolled, or its 128 registers do not hold it)
+#pragma unroll(E4M3 ? 1 : 2)
                             for (int c0 = 0; c0 < TN; c0 += 32) {
                                 float2 s[16];
                                 tmem_ld32(s0 + c0, *reinterpret_cast<float(*)[32]>(&s[0]));
@@ -657,7 +658,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             const float minus = ref == kNegInf ? 0.f : -ref;
                             const float2 minus_2 = make_float2(minus, minus);
                             if (E4M3) tmem_wait_st();
-#pragma unroll
+#pragma unroll(E4M3 ? 1 : 2)
                             for (int c0 = 0; c0 < TN; c0 += 32) {
                                 float2 s[16];
                                 tmem_ld32(s0 + c0, *reinterpret_cast<float(*)[32]>(&s[0]));
