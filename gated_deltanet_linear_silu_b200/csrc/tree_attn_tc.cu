@@ -405,11 +405,14 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             *reinterpret_cast<uint4*>(out + at1) = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16),
                                                                              e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
                         }
+                        if (b == 2 * kSide - 1) {  // (all pieces are in registers: the raw slot is free)
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&B.rempty[rs]);
+                        }
                         if (!C::kOneFull && b % kSide == kSide - 1) publish(&B.full[st + b / kSide]);
                     }
                     if (!ok) break;
                     if (C::kOneFull) publish(&B.full[st]);
-                    if (lane == 0) mbar_arrive(&B.rempty[rs]);  // (publish has synchronised the warp)
                     if (++rs == C::kRawSlots) rs = 0, rpar ^= 1;
                     if ((st += 2) == C::kSlots) st = 0, par ^= 1;
                 } else {
