@@ -18,7 +18,16 @@
 // from a private ring in shared memory that it fills with cp.async; nothing but
 // the end of a segment synchronises the CTA. The order of the contraction over
 // d and of the output's d is free: a lane's fragments are whole 16-byte pieces
-// of a row, whatever elements those are. More rows: tree_attn_tc.cu.
+// of a row, whatever elements those are. More rows: tree_attn_tc.cu. At the
+// border, 16 rows (64 sequences of 8192 tokens, 8 key/value heads of 128, four
+// nodes of four query heads), this kernel takes 241 us and the other 337 from an
+// e4m3 cache, 354 and 362 from a bf16 one; one node: 200 and 327.
+//
+// One node there is 1.1 GB of cache in 192 to 200 us, 5.5 to 5.8 TB/s (84 to 88 %
+// of a copy's rate): HBM is nearly the bound, the rest is the instructions
+// between its loads (60 % of the issue slots). 12 us for one sequence of 1021
+// tokens are latency: two launches, two dependent reads for a page and its rows,
+// and the join.
 //
 // e4m3 values enter the products as f16, exactly, by the hardware conversion
 // (one instruction for two; through bf16 it would take five), and so do the
