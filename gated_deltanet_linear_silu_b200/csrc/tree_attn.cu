@@ -450,6 +450,13 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
         float* buf = reinterpret_cast<float*>(smem);  // [warp][row][D]
         float* mw = buf + kWarps * 8 * NT * D;        // [warp][row]
         float* lw = mw + kWarps * 8 * NT;
+        constexpr int kElems = RB == 64 ? 8 : E4M3 ? 16 : 8;  // of a piece
+        // Place of element d of a row: its 16 bytes exchanged within groups of eight by
+        // the row, so that a warp's stores (eight pieces of four rows) meet every bank.
+        auto place = [](int row, int d) {
+            const int x = row >> 1 & 3;
+            return (((d >> 2) ^ (kElems == 16 ? x : (x & 1) | (x & 2) << 1)) << 2) | (d & 3);
+        };
 #pragma unroll
         for (int g = 0; g < NT; ++g)
 #pragma unroll
@@ -472,13 +479,12 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mw[w * 8 * NT + row]);
                 const float f = ref[g][i] == kNegInf ? 1.f : exp2_approx(ref[g][i] - top);
-                constexpr int kElems = RB == 64 ? 8 : E4M3 ? 16 : 8;  // of a piece
                 float* y = buf + (warp * 8 * NT + row) * D;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     // output tile j: elements 2 j', 2 j' + 1 of the lane's piece j * 2 / kElems
                     const int d = (8 * (2 * j / kElems) + C::piece(r)) * kElems + 2 * j % kElems;
-                    *reinterpret_cast<float2*>(y + d) = make_float2(o[j][g][i] * f, o[j][g][2 + i] * f);
+                    *reinterpret_cast<float2*>(y + place(row, d)) = make_float2(o[j][g][i] * f, o[j][g][2 + i] * f);
                 }
             }
         __syncthreads();
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
             for (int w = 0; w < kWarps; ++w) {
                 const float m = mw[w * 8 * NT + row];
                 lt += m == kNegInf ? lw[w * 8 * NT + row] : lw[w * 8 * NT + row] * exp2_approx(m - mt);
-                const float4 z = *reinterpret_cast<const float4*>(buf + (w * 8 * NT + row) * D + d);
+                const float4 z = *reinterpret_cast<const float4*>(buf + (w * 8 * NT + row) * D + place(row, d));
                 y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
             }
             const int node = row / G, head = hk * G + row % G;
@@ -547,9 +553,21 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int x = blockIdx.y * kWarps + (threadIdx.x >> 5);  // row of the (sequence, head)
     const int rt = x / ROWS, row = x % ROWS;
     pdl_launch_dependents();
-    const Seq seq = load_seq(a, n);  // (inputs of the call: complete before the kernel before let this one start)
-    pdl_wait_previous();
-    if (x >= seq.nodes * G) return;
+    // (inputs of the call: complete before the kernel before let this one start)
+    const Seq seq = load_seq(a, n);
+    const bool live = x < seq.nodes * G;
+    const int64_t t = seq.first + x / G;
+    const int head = hk * G + x % G;
+    constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4s of a lane
+    float4 gate[V];
+    if (a.gate && live) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (4 * lane + 128 * v < D)
+                gate[v] = load4(static_cast<const uint16_t*>(a.gate) + (t * a.H + head) * D + 4 * lane + 128 * v);
+    }
+    pdl_wait_previous();  // (every warp: what follows this kernel counts on the one before it being done)
+    if (!live) return;
     const UnitParts parts = *unit_parts(a, rt, n, hk);
     const int c0 = parts.first >> 1;
     // one CTA had the whole unit and wrote it (or the kernel before gave up: then these are anything)
@@ -557,7 +575,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int count = parts.last - c0 + 1;
     const float* partials = partial_base(a);
     auto part = [&](int i) { return partials + (i == 0 ? parts.first : 2 * (c0 + i)) * slot_floats(D, a.slot_rows); };
-    constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4s of a lane
     constexpr int kAhead = 8 / V;                 // parts whose rows are requested together
     auto load = [&](int i0, float4 (&z)[kAhead][V]) {
 #pragma unroll
@@ -607,8 +624,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     lt = warp_sum(lt);
     const bool empty = mt == kNegInf && lt == 0.f;
     const float inv = empty ? 0.f : 1.f / lt;
-    const int64_t t = seq.first + x / G;
-    const int head = hk * G + x % G;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int d = 4 * lane + 128 * v;
@@ -616,7 +631,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
         const int64_t out = (t * a.H + head) * D + d;
         float4 z = make_float4(y[v].x * inv, y[v].y * inv, y[v].z * inv, y[v].w * inv);
         if (a.gate) {
-            const float4 g = load4(static_cast<const uint16_t*>(a.gate) + out);
+            const float4 g = gate[v];
             z.x /= 1.f + __expf(-g.x); z.y /= 1.f + __expf(-g.y);
             z.z /= 1.f + __expf(-g.z); z.w /= 1.f + __expf(-g.w);
         }

@@ -141,6 +141,7 @@ __device__ __forceinline__ int64_t seq_tiles(const Seq& q) {
 struct Share {
     int64_t begin, end, n_start;
     int rt, n;
+    Seq seq;  // of sequence n
 };
 
 // Every thread of the CTA takes part (it synchronises the CTA).
@@ -149,8 +150,59 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
     constexpr int W = THREADS / 32;
     __shared__ unsigned long long totals[kMaxRowTiles];
     __shared__ int64_t scan[W], found[2];
+    __shared__ Seq found_seq;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int N = a.p.N, RT = a.row_tiles;
+    Share s;
+    s.begin = s.end = 0;
+    s.rt = RT;
+    s.n = N;
+    s.n_start = 0;
+    auto scan_warp = [&](int64_t x) {  // sum of the warp's values up to this lane's
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scan[warp] = x;
+        return x;
+    };
+    if (RT == 1 && N <= THREADS) {
+        // The usual step, a sequence per thread and one line: a single pass. With one
+        // sequence of 1021 tokens the way below takes 1.3 us more of the kernel's 7.
+        Seq q;
+        int64_t own = 0;
+        if (tid < N) {
+            q = load_seq(a, tid);
+            if (q.bad && blockIdx.x == 0) set_status(a.status, kStatusBadSeqlens);
+            if (q.nodes > 0) own = a.c.Hk * seq_tiles<TN>(q);
+        }
+        int64_t start = scan_warp(own) - own;
+        __syncthreads();
+        int64_t line = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) start += scan[w];
+            line += scan[w];
+        }
+        const int64_t shares = line < (int64_t)gridDim.x ? line : (int64_t)gridDim.x, c = blockIdx.x;
+        s.rt = 0;
+        if (c < shares) {
+            s.begin = quotient(c * line, shares);
+            s.end = quotient((c + 1) * line, shares);
+            if (start <= s.begin && s.begin < start + own) {
+                found[0] = tid;
+                found[1] = start;
+                found_seq = q;
+            }
+        }
+        __syncthreads();
+        if (s.begin == s.end) return s;
+        s.n = (int)found[0];
+        s.n_start = found[1];
+        s.seq = found_seq;
+        return s;
+    }
     if (tid < RT) totals[tid] = 0;
     if (tid == 0) found[0] = N;
     __syncthreads();
@@ -168,11 +220,6 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
         all += run;
         active += run > 0;
     }
-    Share s;
-    s.begin = s.end = 0;
-    s.rt = RT;
-    s.n = N;
-    s.n_start = 0;
     {
         int64_t line = run;  // line 0
         int cta = 0;
@@ -198,13 +245,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
             const Seq q = load_seq(a, n);
             if (seq_row_tiles<ROWS>(a, q) > s.rt) own = a.c.Hk * seq_tiles<TN>(q);
         }
-        int64_t x = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) scan[warp] = x;
+        const int64_t x = scan_warp(own);
         __syncthreads();
         int64_t pre = before;
         for (int w = 0; w < W; ++w) {
@@ -221,6 +262,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs& a) {
     }
     s.n = (int)found[0];
     s.n_start = found[1];
+    s.seq = load_seq(a, s.n);
     return s;
 }
 
@@ -251,7 +293,7 @@ __device__ __forceinline__ bool first_segment(const TreeArgs& a, const Share& s,
     if (s.begin == s.end) return false;
     g.n = s.n;
     g.n_start = s.n_start;
-    g.seq = load_seq(a, g.n);
+    g.seq = s.seq;
     place_segment<ROWS, TN>(a, s, s.begin, g);
     return true;
 }

@@ -201,9 +201,6 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (warp-uniform to the compiler)
     const int G = a.H / a.c.Hk;
     const uint64_t wlim = a.wait_ns;
-    pdl_wait_previous();  // (before its dependents, which read the call's inputs at once)
-    pdl_launch_dependents();
-
     if (tid == 0) {
         for (int i = 0; i < 12; ++i) {
             mbar_init(&B.full[i], kConvWarps);
@@ -231,6 +228,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         for (int i = 0; i < kSoftWarps; ++i) B.gave_up[i] = 0;
     }
     if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
+    pdl_wait_previous();  // (before its dependents, which read the call's inputs at once)
+    pdl_launch_dependents();
     tc_fence_before();
     const Share share = find_share<kTcRows, TN, C::kThreads>(a);  // (synchronises the CTA)
     tc_fence_after();
@@ -549,14 +548,16 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
             if (busy) {
                 const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.ld_q +
                                                                  (int64_t)head * D + half * (D / 2));
+                uint4 u[D / 16];  // (all of it at once: nothing else hides the reads' latency here)
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) u[e] = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
                 float down = 1.f;
                 if (E4M3) {
                     // as f16, the row scaled by a power of two that puts its largest element in [1, 2)
                     uint32_t big = 0;
-#pragma unroll 4
+#pragma unroll
                     for (int e = 0; e < D / 16; ++e) {
-                        const uint4 u = live ? qp[e] : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) big = max(big, max(w[y] & 0x7FFFu, w[y] >> 16 & 0x7FFFu));
                     }
@@ -568,13 +569,13 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     down = __uint_as_float((254u - ex) << 23);
                     mul *= __uint_as_float(ex << 23);
                 }
-#pragma unroll 1
+#pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint4 u = live ? qp[c0 / 8 + e] : make_uint4(0, 0, 0, 0);
-                        w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
+                        const uint4 x = u[c0 / 8 + e];
+                        w[4 * e] = x.x; w[4 * e + 1] = x.y; w[4 * e + 2] = x.z; w[4 * e + 3] = x.w;
                     }
                     if (E4M3) {
 #pragma unroll
