@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int count = parts.last - c0 + 1;
     const float* partials = partial_base(a);
     auto part = [&](int i) { return partials + (i == 0 ? parts.first : 2 * (c0 + i)) * slot_floats(D, a.slot_rows); };
-    constexpr int kAhead = 8 / V;                 // parts whose rows are requested together
+    constexpr int kAhead = 16 / V;                // parts whose rows are requested together
     auto load = [&](int i0, float4 (&z)[kAhead][V]) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
