@@ -544,13 +544,14 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
     }
 }
 
-// Joins the partials of the units that span CTAs: one warp per row.
-template <int D, int ROWS, int TN>
-__global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
-    const int lane = threadIdx.x & 31;
+// Joins the partials of the units that span CTAs: a warp per row, or SPLIT warps,
+// a stretch of the partials each.
+template <int D, int ROWS, int TN, int SPLIT>
+__global__ void __launch_bounds__(SPLIT > 1 ? 32 * SPLIT : kThreads) join_kernel(TreeArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = blockIdx.x / a.c.Hk, hk = blockIdx.x % a.c.Hk;
     const int G = a.H / a.c.Hk;
-    const int x = blockIdx.y * kWarps + (threadIdx.x >> 5);  // row of the (sequence, head)
+    const int x = SPLIT > 1 ? blockIdx.y : blockIdx.y * kWarps + warp;  // row of the (sequence, head)
     const int rt = x / ROWS, row = x % ROWS;
     pdl_launch_dependents();
     // (inputs of the call: complete before the kernel before let this one start)
@@ -572,9 +573,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
     const int c0 = parts.first >> 1;
     // one CTA had the whole unit and wrote it (or the kernel before gave up: then these are anything)
     if (parts.first < 0 || parts.last <= c0 || parts.last >= a.grid) return;
-    const int count = parts.last - c0 + 1;
+    const int all = parts.last - c0 + 1, from = SPLIT > 1 ? all * warp / SPLIT : 0;
+    const int count = SPLIT > 1 ? all * (warp + 1) / SPLIT - from : all;  // of this warp
     const float* partials = partial_base(a);
-    auto part = [&](int i) { return partials + (i == 0 ? parts.first : 2 * (c0 + i)) * slot_floats(D, a.slot_rows); };
+    auto part = [&](int i) {
+        return partials + (from + i == 0 ? parts.first : 2 * (c0 + from + i)) * slot_floats(D, a.slot_rows);
+    };
     constexpr int kAhead = 16 / V;                // parts whose rows are requested together
     auto load = [&](int i0, float4 (&z)[kAhead][V]) {
 #pragma unroll
@@ -622,6 +626,37 @@ __global__ void __launch_bounds__(kThreads) join_kernel(TreeArgs a) {
         }
     }
     lt = warp_sum(lt);
+    if constexpr (SPLIT > 1) {  // the stretches, in order
+        __shared__ float4 sums[SPLIT][D / 4];
+        __shared__ float tops[SPLIT], totals[SPLIT];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (4 * lane + 128 * v < D) sums[warp][lane + 32 * v] = y[v];
+        if (lane == 0) {
+            tops[warp] = mt;
+            totals[warp] = lt;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        mt = kNegInf;
+#pragma unroll
+        for (int w = 0; w < SPLIT; ++w) mt = fmaxf(mt, tops[w]);
+        lt = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < SPLIT; ++w) {
+            const float f = tops[w] == kNegInf ? 1.f : exp2_approx(tops[w] - mt);
+            lt = fmaf(totals[w], f, lt);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (4 * lane + 128 * v >= D) continue;
+                const float4 u = sums[w][lane + 32 * v];
+                y[v].x = fmaf(u.x, f, y[v].x); y[v].y = fmaf(u.y, f, y[v].y);
+                y[v].z = fmaf(u.z, f, y[v].z); y[v].w = fmaf(u.w, f, y[v].w);
+            }
+        }
+    }
     const bool empty = mt == kNegInf && lt == 0.f;
     const float inv = empty ? 0.f : 1.f / lt;
 #pragma unroll
@@ -675,11 +710,20 @@ cudaError_t launch_mma(const TreeArgs& a, cudaStream_t s) {
 template <int D, bool E4M3>
 cudaError_t launch_config(const TreeArgs& a, bool tc, cudaStream_t s) {
     const int rows = a.max_nodes * (a.H / a.c.Hk);
-    const dim3 join(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps);
     const cudaError_t e = tc ? launch_tree_tc(a, s) : rows <= 8 ? launch_mma<D, E4M3, 1>(a, s) : launch_mma<D, E4M3, 2>(a, s);
     if (e != cudaSuccess) return e;
-    if (tc) return launch_pdl(join_kernel<D, kTcRows, kTcTile>, join, dim3(kThreads), 0, s, a);
-    return launch_pdl(join_kernel<D, kRows, kTile>, join, dim3(kThreads), 0, s, a);
+    // Few long units have many partials each, and few rows to share them: eight warps
+    // to a row then. One sequence, one node, 2 heads of 256, with a warp and with eight: 16
+    // partials 9.3 and 9.7 us, 32 partials 10.8 and 9.3, 222 (30000 tokens) 34.3 and 18.6.
+    if (a.grid > (int64_t)20 * a.row_tiles * a.p.N * a.c.Hk) {
+        constexpr int kSplit = 8;
+        const dim3 join(a.p.N * a.c.Hk, rows);
+        if (tc) return launch_pdl(join_kernel<D, kTcRows, kTcTile, kSplit>, join, dim3(32 * kSplit), 0, s, a);
+        return launch_pdl(join_kernel<D, kRows, kTile, kSplit>, join, dim3(32 * kSplit), 0, s, a);
+    }
+    const dim3 join(a.p.N * a.c.Hk, (rows + kWarps - 1) / kWarps);
+    if (tc) return launch_pdl(join_kernel<D, kTcRows, kTcTile, 1>, join, dim3(kThreads), 0, s, a);
+    return launch_pdl(join_kernel<D, kRows, kTile, 1>, join, dim3(kThreads), 0, s, a);
 }
 
 template <int D>

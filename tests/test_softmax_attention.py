@@ -548,6 +548,30 @@ def test_tree_attention_long(held):
 
 
 @pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D,nodes", [(64, 1), (64, 9), (128, 1), (128, 5), (256, 1), (256, 3), (256, 6)])
+def test_tree_attention_of_one_sequence(held, D, nodes):
+    """One sequence alone: a few tiles for each of many CTAs, tens of partials to
+    a row, with the gate."""
+    pool = Pool([2500], [nodes], 2, D, 32, held, fill=85)
+    q, gate = (rnd(s, nodes, 8, D, dtype=BF).to(DEV) for s in (86, 87))
+    mask = trees([nodes], 11)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=nodes, mask=mask.to(DEV), gate=gate, return_lse=True)
+    check_attention(pool, q, o, lse, mask, D ** -0.5, gate=gate)
+
+
+@pytest.mark.parametrize("N,nodes", [(128, 1), (129, 1), (300, 2), (512, 9), (513, 9), (700, 9)])
+def test_tree_attention_of_many_sequences(N, nodes):
+    """More sequences than a CTA has threads, and as many; empty ones among them."""
+    g = torch.Generator().manual_seed(N)
+    counts = [min(int(c), nodes) for c in torch.randint(0, nodes + 1, (N,), generator=g)]
+    lens = [c + int(x) for c, x in zip(counts, torch.randint(0, 70, (N,), generator=g))]
+    pool = Pool(lens, counts, 1, 64, 16, F8, fill=88)
+    q = rnd(89, sum(counts), 2, 64, dtype=BF).to(DEV)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=nodes, return_lse=True)
+    check_attention(pool, q, o, lse, None, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("held", [F8, BF])
 @pytest.mark.parametrize("D,G,nodes", [(64, 8, 40), (128, 4, 7), (256, 4, 17), (128, 16, 20)])
 def test_tree_attention_long_with_many_rows(held, D, G, nodes):
     """The same with more rows than one group of eight or sixteen: hundreds of
