@@ -23,11 +23,10 @@
 // nodes of four query heads), this kernel takes 241 us and the other 337 from an
 // e4m3 cache, 354 and 362 from a bf16 one; one node: 200 and 327.
 //
-// One node there is 1.1 GB of cache in 192 to 200 us, 5.5 to 5.8 TB/s (84 to 88 %
+// One node there is 1.1 GB of cache in 184 to 194 us, 5.7 to 6.0 TB/s (87 to 92 %
 // of a copy's rate): HBM is nearly the bound, the rest is the instructions
-// between its loads (60 % of the issue slots). 12 us for one sequence of 1021
-// tokens are latency: two launches, two dependent reads for a page and its rows,
-// and the join.
+// between its loads. 9.8 us for one sequence of 1021 tokens are latency: bounds and
+// shares 1 us, a page's id and its rows 3, the four warps' sums 1, the join 3.5.
 //
 // e4m3 values enter the products as f16, exactly, by the hardware conversion
 // (one instruction for two; through bf16 it would take five), and so do the
@@ -579,7 +578,9 @@ __global__ void __launch_bounds__(SPLIT > 1 ? 32 * SPLIT : kThreads) join_kernel
     auto part = [&](int i) {
         return partials + (from + i == 0 ? parts.first : 2 * (c0 + from + i)) * slot_floats(D, a.slot_rows);
     };
-    constexpr int kAhead = 16 / V;                // parts whose rows are requested together
+    // Parts whose rows are requested together. Where units have few of them, more only
+    // take registers (8 x 32768 tokens, 64 nodes: 294 us with 8 of d = 128, 301 with 16).
+    constexpr int kAhead = (SPLIT > 1 ? 16 : 8) / V;
     auto load = [&](int i0, float4 (&z)[kAhead][V]) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -714,8 +715,8 @@ cudaError_t launch_config(const TreeArgs& a, bool tc, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // Few long units have many partials each, and few rows to share them: eight warps
     // to a row then. One sequence, one node, 2 heads of 256, with a warp and with eight: 16
-    // partials 9.3 and 9.7 us, 32 partials 10.8 and 9.3, 222 (30000 tokens) 34.3 and 18.6.
-    if (a.grid > (int64_t)20 * a.row_tiles * a.p.N * a.c.Hk) {
+    // partials 10.6 and 9.8 us, 32 partials 10.8 and 9.3, 222 (30000 tokens) 34.3 and 18.6.
+    if (a.grid > (int64_t)12 * a.row_tiles * a.p.N * a.c.Hk) {
         constexpr int kSplit = 8;
         const dim3 join(a.p.N * a.c.Hk, rows);
         if (tc) return launch_pdl(join_kernel<D, kTcRows, kTcTile, kSplit>, join, dim3(32 * kSplit), 0, s, a);
