@@ -305,6 +305,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         break;
                     }
                     if (by_hand(seg, tile)) {  // (the converters walk only these: the slots' phases are followed here)
+                        // the last copy into this slot has landed (its products are done, or the slot
+                        // would not be free), and the phase now begun is the converters'
+                        last_full &= ~(1u << st);
                         if (lane == 0) mbar_arrive(&B.hand[st]);
                     } else {
                         uint8_t* dst = sm + st * C::kSlot;
