@@ -40,7 +40,9 @@
 // 900 their waits and hand-overs (shared memory alone needs 1200), and 8 us of
 // bounds, queries and output for each (sequence, head) that a CTA takes part in.
 //
-// Every wait is bounded (gdn_set_wait_limit_ns).
+// Every wait between warps is bounded by gdn_set_wait_limit_ns, and the two at the
+// end, for the copies and the products in flight, by kDrainWaitNs: nothing may land
+// in the CTA's memory after it is gone. Either kind reports that it ran out.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -340,7 +342,8 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         // no copy may land after the CTA is gone
         if (lane == 0)
             for (int x = 0; x < (E4M3 ? C::kRawSlots : C::kSlots); ++x)
-                if ((last_full >> x) & 1) mbar_wait(E4M3 ? &B.rfull[x] : &B.full[x], (last_par >> x) & 1, kDrainWaitNs);
+                if ((last_full >> x) & 1 && !mbar_wait(E4M3 ? &B.rfull[x] : &B.full[x], (last_par >> x) & 1, kDrainWaitNs))
+                    set_status(a.status, kStatusTimeout);
         __syncwarp();
     } else if (E4M3 && warp >= C::kScaleWarp0) {
         // ================================================================= scales
@@ -526,7 +529,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
         if (!ok && lane == 0) fail();
         if (elect_one()) mma_commit(&B.drain);
         __syncwarp();
-        mbar_wait(&B.drain, 0, kDrainWaitNs);
+        if (!mbar_wait(&B.drain, 0, kDrainWaitNs)) set_status(a.status, kStatusTimeout);
     } else {
         // ================================================================= softmax
         const int quarter = warp & 3, half = warp >> 2;  // half: of the columns, or the group
