@@ -415,11 +415,14 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 }
                 if (!E4M3 && drafted) {
                     // a drafted value that is not finite must not reach the rows that do not see it:
-                    // zero here, added to the others at the end of the segment
+                    // zero here, added to the others at the end of the segment (the context's, which
+                    // every row sees, stay)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 4; ++x) {
+                        if (pos + 8 * (x >> 1) + C::token(2 * c + (x & 1)) < base) continue;
 #pragma unroll
                         for (int w = 0; w < W; ++w) odd |= zero_non_finite(v[x][w]);
+                    }
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {

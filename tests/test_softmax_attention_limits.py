@@ -51,3 +51,29 @@ def test_tree_attention_ends_inside_a_stretch(lens, nodes, H, Hk, D, held):
     gdn.check_device_status(DEV)
     small = sorted(range(len(lens)), key=lambda n: lens[n] * nodes[n])
     check_attention(pool, q, o, lse, mask, D ** -0.5, rows=[small[0], small[len(small) // 3]])
+
+
+# ---------------------------------------------------------------- inputs that are not finite
+
+@pytest.mark.parametrize("heads,D,lens,c", [(2, 128, 44, 8), (1, 64, 3007, 5), (4, 256, 45, 3), (2, 256, 641, 2),
+                                            (4, 128, 44, 8), (8, 64, 3007, 5), (16, 256, 641, 2), (8, 256, 45, 3)])
+def test_tree_attention_non_finite_context(heads, D, lens, c):
+    """Context values that are not finite reach every row, also where their tokens
+    stand right before the draft (which is held back there); up to sixteen query
+    rows and more."""
+    pool = Pool([lens], [c], 1, D, 16, BF, fill=151)
+    base = lens - c
+    for at, element, value in ((base - 1, 3, math.inf), (base - 2, 5, math.nan), (base // 2, 9, -math.inf)):
+        page, row = (int(x) for x in pool.spots(0, at))
+        pool.cache.v[page, 0, row, element] = value
+    q = rnd(152, c, heads, D, dtype=BF).to(DEV)
+    mask = trees([c], 13)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=c, mask=mask.to(DEV), return_lse=True)
+    assert (o[..., 3] == math.inf).all() and o[..., 5].isnan().all() and (o[..., 9] == -math.inf).all()
+    rest = [e for e in range(D) if e not in (3, 5, 9)]
+    assert o[..., rest].isfinite().all() and lse.isfinite().all()
+    k, v = (pool.rows(0, range(lens), name) for name in ("k", "v"))
+    want, z, mass, size = ref.attention(q.cpu(), k, v.nan_to_num(0, 0, 0), base, mask, D ** -0.5)
+    s, u = ((D + 8) * E * size + 8 * E)[..., None], half_step(BF)
+    close(o[..., rest], want[..., rest], ((u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())[..., rest])
+    close(lse, z, s[..., 0] + 2.0 ** -9 + 8 * E * z.abs())
