@@ -77,3 +77,147 @@ def test_tree_attention_non_finite_context(heads, D, lens, c):
     s, u = ((D + 8) * E * size + 8 * E)[..., None], half_step(BF)
     close(o[..., rest], want[..., rest], ((u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())[..., rest])
     close(lse, z, s[..., 0] + 2.0 ** -9 + 8 * E * z.abs())
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("length", [40, 72, 128, 5000])
+def test_many_rows_non_finite_behind_the_mask(held, D, length):
+    """test_tree_attention_non_finite_behind_the_mask with 32 query rows: NaN and
+    infinities in a node that a row does not see do not reach it; in one that it
+    sees, they do. Rows behind the sequence hold NaN as well."""
+    c = 8
+    pool = Pool([length], [c], 1, D, 16, held, fill=161)
+    base = length - c
+
+    def put(name, node, value, element=None):
+        page, row = (int(x) for x in pool.spots(0, base + node))
+        if held == F8:
+            getattr(pool.cache, name + "_scale")[page, :, row] = value
+        else:
+            getattr(pool.cache, name)[page, :, row, slice(None) if element is None else element] = value
+
+    mask = torch.tensor([0b1, 0b11, 0b101, 0b1001, 0b10001, 0b110001, 0b1010001, 0b10111001], dtype=torch.int64)
+    q = rnd(162, c, 4, D, dtype=BF).to(DEV)
+    clean, clean_lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=c, mask=mask.to(DEV), return_lse=True)
+    check_attention(pool, q, clean, clean_lse, mask, D ** -0.5)
+    put("v", 1, math.nan)
+    put("k", 2, math.nan)
+    if held == BF:
+        put("v", 3, math.inf, 33)
+    else:
+        put("k", 1, math.inf)  # a scale that no write leaves, in the node whose values are NaN
+    if length % 16:
+        page = pool.ids[0, length // 16]
+        for name in ("k", "v"):
+            if held == F8:
+                getattr(pool.cache, name + "_scale")[page, :, length % 16:] = math.nan
+                getattr(pool.cache, name).view(torch.uint8)[page, :, length % 16:] = 0x7F
+            else:
+                getattr(pool.cache, name)[page, :, length % 16:] = math.nan
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=c, mask=mask.to(DEV), return_lse=True)
+    assert o[1].isnan().all() and o[2].isnan().all() and lse[2].isnan().all()
+    same = [0, 3, 4, 5, 6, 7] if held == F8 else [0, 4, 5, 6]
+    assert torch.equal(o[same], clean[same]) and torch.equal(lse[same], clean_lse[same])
+    if held == BF:
+        assert lse[1].isfinite().all()
+        for t in (3, 7):
+            assert (o[t, :, 33] == math.inf).all() and torch.equal(lse[t], clean_lse[t])
+            rest = [e for e in range(D) if e != 33]
+            assert torch.equal(o[t][:, rest], clean[t][:, rest])
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_extreme_scores(held, D):
+    """test_tree_attention_extreme_scores with 32 query rows. A row's numerators
+    are off by at most 2 s, s its scores' error; where that passes one they may be
+    anything between none and all, but stay weights: the output is bounded by the
+    largest value."""
+    pool = Pool([300, 70], [4, 4], 1, D, 16, held, fill=163)
+    q = rnd(164, 8, 8, D, dtype=BF, scale=300.0).to(DEV)
+    mask = trees([4, 4], 14)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=4, mask=mask.to(DEV), scale=30.0, return_lse=True)
+    for n, (l, rows) in enumerate(((300, slice(0, 4)), (70, slice(4, 8)))):
+        k, v = pool.rows(n, range(l), "k"), pool.rows(n, range(l), "v")
+        want, z, mass, size = ref.attention(q[rows].cpu(), k, v, l - 4, mask[rows], 30.0)
+        assert (o[rows].cpu().double().abs() <= v.abs().amax() * (1 + 2.0 ** -6)).all()
+        assert ((lse[rows].cpu().double() - z).abs() <= (D + 16) * E * size + 8 * E * z.abs() + 2.0 ** -9).all()
+    if held == BF:  # every key at minus infinity
+        pool.cache.k[:] = 0
+        pool.cache.k[..., 0] = -math.inf
+        q = torch.zeros(8, 8, D, dtype=BF, device=DEV)
+        q[..., 0] = 1
+        o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=4, mask=mask.to(DEV), return_lse=True)
+        assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("D", [128, 256])
+def test_many_rows_growing_scores(held, D):
+    """Scores that rise and fall by hundreds along the context: the running
+    reference moves many times, on either parity of the tiles."""
+    L, c = 2100, 6
+    pool = Pool([L], [c], 1, D, 32, held)
+    k, v = (rnd(165 + i, L, 1, D) for i in (0, 1))
+    wave = torch.cumsum(torch.where(torch.rand(L, generator=torch.Generator().manual_seed(3)) < 0.5, -1.0, 1.0), 0)
+    k[:, 0, 0] = wave * 8 + torch.arange(L) / 16
+    whole = (pool.table, pool.lens, torch.tensor([0, L], dtype=torch.int32, device=DEV))
+    gdn.kv_cache_write(k.to(DEV), v.to(DEV), pool.cache, *whole)
+    q = rnd(167, c, 4, D, dtype=BF)
+    q[..., 0] = 16
+    q = q.to(DEV)
+    mask = trees([c], 15)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=c, mask=mask.to(DEV), return_lse=True)
+    check_attention(pool, q, o, lse, mask, D ** -0.5)
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("page", [16, 64])
+def test_many_rows_bad_sequences(held, page):
+    """test_tree_attention_bad_sequences with 32 query rows and more: what the
+    loader and the converters do about a page that does not exist, in the context
+    and in the draft."""
+    for what in ("nodes", "short", "page", "last"):
+        pool = Pool([150, 260], [8, 9], 1, 64, page, held, fill=171)
+        q = rnd(172, 17, 8, 64, dtype=BF).to(DEV)
+        if what == "short":
+            pool.lens[0] = 100000
+        if what == "page":
+            pool.table[0, 1] = 1 << 30
+        if what == "last":
+            pool.table[0, 149 // page] = -1
+        if what == "nodes":
+            pool.cu[1], pool.cu[2] = 8, 8 + 40
+            q = rnd(172, 48, 8, 64, dtype=BF).to(DEV)
+            pool.host_lens, pool.counts = [150, 260], [8, 40]
+        out = torch.full(q.shape, 7.0, dtype=BF, device=DEV)
+        o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=9, out=out, return_lse=True)
+        status_bad()
+        if what == "nodes":
+            assert (o[8:] == 7).all()
+        elif what == "short":
+            assert (o[:8] == 7).all()
+        check_attention(pool, q, o, lse, None, 0.125, rows=[0 if what == "nodes" else 1])
+
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("nodes,H", [(2, 8), (5, 32)])
+def test_many_pages_past_32_bits(held, nodes, H):
+    """Rows whose byte and element offsets pass 2^32, both kernels and cache types."""
+    P, page, Hk, D = 18000, 128, 8, 256
+    shape = (P, Hk, page, D)
+    cache = gdn.KVCache(*(torch.empty(shape, dtype=held, device=DEV) for _ in range(2)),
+                        *((torch.empty(shape[:3], dtype=F32, device=DEV) for _ in range(2)) if held == F8 else ()))
+    table = torch.tensor([[P - 1, 3, P - 2]], dtype=torch.int32, device=DEV)
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([300], [0, 300]))
+    k, v = (rnd(s, 300, Hk, D, dtype=BF) for s in (181, 182))
+    gdn.kv_cache_write(k.to(DEV), v.to(DEV), cache, table, lens, cu)
+    a, b = gdn.kv_cache_read(cache, table, lens, cu, n_tokens=300, dtype=F32)
+    q = rnd(183, nodes, H, D, dtype=BF).to(DEV)
+    draft = torch.tensor([0, nodes], dtype=torch.int32, device=DEV)
+    o = gdn.tree_attention(q, cache, table, lens, draft, max_nodes=nodes)
+    want, z, mass, size = ref.attention(q.cpu(), a.cpu(), b.cpu(), 300 - nodes, [(2 << i) - 1 for i in range(nodes)], D ** -0.5)
+    s = ((D + 8) * E * size + 8 * E)[..., None]
+    u = half_step(BF)
+    close(o, want, (u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())
