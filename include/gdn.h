@@ -484,6 +484,9 @@ GDN_API gdn_status_t gdn_gated_rmsnorm(const void* y, const void* z, const float
  * concerned are skipped (gdn_tree_attention: see there) and everything else is
  * done. Sequences may share pages
  * that a call only reads; a page that a call writes belongs to one sequence.
+ * What these calls write (outputs, the workspace, a cache that they write to) must
+ * not overlap what they read, nor one another, but for the in-place forms that
+ * gdn_qk_norm_rope allows: GDN_ERR_INVALID_ARG.
  */
 typedef struct {
     void* k;
@@ -556,8 +559,7 @@ GDN_API gdn_status_t gdn_kv_read(const gdn_kv_cache_t* cache, const int32_t* pag
  * in place, and new_seq_lens[n] is the length up to the last accepted node. A
  * row of `accepted` [N, M] int32 holds increasing node numbers and, behind
  * them, -1s (any negative number); one that does not moves nothing, keeps
- * seq_lens[n] and sets the device status word. new_seq_lens must not be
- * seq_lens. Supported: M <= 64.
+ * seq_lens[n] and sets the device status word. Supported: M <= 64.
  */
 GDN_API gdn_status_t gdn_kv_accept(const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,
                                    const int32_t* seq_lens, const int32_t* cu_seqlens, int N,

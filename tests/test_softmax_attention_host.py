@@ -10,7 +10,7 @@ import gated_deltanet_linear_silu_b200 as gdn
 from gated_deltanet_linear_silu_b200 import build as gbuild
 from gated_deltanet_linear_silu_b200.softmax_attention import _CacheStruct
 
-OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+OK, INVALID, UNSUPPORTED, WORKSPACE, NO_DEVICE = 0, 1, 2, 3, 4
 A = 1 << 20  # aligned, never dereferenced: validation fails first
 B = 1 << 21
 NAN = float("nan")
@@ -158,6 +158,74 @@ def test_workspace_size_of_unsupported_arguments(L, kw):
     a = dict(N=1, H=4, max_nodes=2)
     a.update(kw)
     assert L.gdn_tree_attention_workspace_size(cache(), *a.values()) == 0
+
+
+def at(n):
+    """Addresses 16 MB apart, for buffers that share nothing."""
+    return n << 24
+
+
+# a cache of 4 pages of 16 rows of 2 heads of 64: 8192 bytes of values, 512 of scales
+APART_CACHE = dict(k=at(10), v=at(11), k_scale=at(12), v_scale=at(13))
+# queries [3, 4, 64] bf16: 1536 bytes; keys [3, 2, 64]: 768; fp32 weights 256
+APART = dict(cache=cache(**APART_CACHE), table=at(14), lens=at(15), cu=at(16), q=at(1), k=at(2), v=at(3), qw=at(4), kw=at(5),
+             pos=at(6), f=at(7), qo=at(8), ko=at(9), path=at(17), out=at(18), mask=at(19), gate=at(20), o=at(21),
+             lse=at(22), ws=at(23))
+
+
+def apart(call, L, **kw):
+    a = dict(APART, **({"bytes": 1 << 23} if call is attend else {}), **kw)
+    if call is norm_rope:
+        for x in ("cache", "table", "lens", "cu", "v", "path", "out", "mask", "gate", "o", "lse", "ws"):
+            del a[x]
+    if call is read:
+        a["k"], a["v"] = kw.get("k", at(24)), kw.get("v", at(25))
+    return call(L, **a)
+
+
+OVERLAPPING = [
+    (norm_rope, dict(qo=at(2))), (norm_rope, dict(ko=at(1))), (norm_rope, dict(qo=at(1) + 16)), (norm_rope, dict(qo=at(1) - 16)),
+    (norm_rope, dict(ko=at(2) + 752)), (norm_rope, dict(ko=at(8) + 1520)), (norm_rope, dict(ko=at(8) - 752)),
+    (norm_rope, dict(ko=at(8))), (norm_rope, dict(qw=at(8) + 1520)), (norm_rope, dict(kw=at(9) + 752)),
+    (norm_rope, dict(pos=at(8) + 8)), (norm_rope, dict(f=at(9) - 120)),
+    (norm_rope, dict(ldq=4096, qo=at(1) + 16384 - 16 + 512 - 16)),  # rows 8192 bytes apart: the end of the last
+    (norm_rope, dict(ldk=4096, qo=at(2) + 8192 - 1520)),            # the start of the second
+    (rope_cache, dict(qo=at(2))), (rope_cache, dict(qo=at(3) + 752)), (rope_cache, dict(qo=at(1) + 512)),
+    (rope_cache, dict(qo=at(10) + 8176)), (rope_cache, dict(qo=at(13))), (rope_cache, dict(qo=at(14))),
+    (rope_cache, dict(q=at(10))), (rope_cache, dict(k=at(11) + 512)), (rope_cache, dict(v=at(12) - 752)),
+    (rope_cache, dict(lens=at(10))), (rope_cache, dict(pos=at(8) + 4)),
+    (write, dict(k=at(10))), (write, dict(v=at(11) + 8176)), (write, dict(v=at(10) - 752)), (write, dict(table=at(12) + 508)),
+    (write, dict(cache=cache(**{**APART_CACHE, "v": at(10)}))), (write, dict(cache=cache(**{**APART_CACHE, "k_scale": at(10)}))),
+    (read, dict(k=at(25))), (read, dict(k=at(25) + 752)), (read, dict(v=at(24) + 752)), (read, dict(k=at(10))),
+    (read, dict(v=at(13) + 496)), (read, dict(lens=at(24) + 4)),
+    (accept, dict(out=at(15))), (accept, dict(out=at(16) + 4)), (accept, dict(out=at(17) + 12)), (accept, dict(out=at(14) + 4)),
+    (accept, dict(out=at(10) + 64)), (accept, dict(path=at(11) + 64)), (accept, dict(N=2, out=at(15) + 4)),
+    (accept, dict(N=2, out=at(15) - 4)),
+    (attend, dict(o=at(1))), (attend, dict(o=at(1) + 1520)), (attend, dict(gate=at(21))), (attend, dict(gate=at(21) - 1520)),
+    (attend, dict(mask=at(21) + 8)), (attend, dict(lse=at(21) + 1532)), (attend, dict(lse=at(1))), (attend, dict(lse=at(16))),
+    (attend, dict(o=at(11) + 4096)), (attend, dict(ws=at(21))), (attend, dict(ws=at(1))), (attend, dict(ws=at(22))),
+    (attend, dict(ws=at(10) - 256)), (attend, dict(lens=at(23) + 512)),
+]
+BESIDE = [  # what lies right beside, or in place
+    (norm_rope, {}), (norm_rope, dict(qo=at(1), ko=at(2))), (norm_rope, dict(qo=at(2) - 1536, ko=at(2))),
+    (norm_rope, dict(ldq=4096, qo=at(1) + 512)), (norm_rope, dict(ldq=4096, ko=at(1) + 16384 - 768)),
+    (norm_rope, dict(T=1, ko=at(1) + 512)), (norm_rope, dict(T=1, ldq=1024, ko=at(1) + 512)),
+    (rope_cache, {}), (rope_cache, dict(qo=at(1))), (rope_cache, dict(k=at(1) + 512, v=at(1) + 768, ldq=512, ldk=512, ldv=512)),
+    (write, {}), (write, dict(k=at(3) + 256, ldk=256, ldv=256)), (write, dict(v=at(10) + 8192)), (read, {}),
+    (read, dict(k=at(25) - 768)), (accept, {}), (accept, dict(out=at(15) + 4)), (attend, {}), (attend, dict(o=at(1) + 1536)),
+    (attend, dict(cache=cache(k=at(10), v=at(10), k_scale=at(12), v_scale=at(12)))), (attend, dict(gate=None, lse=None, mask=None)),
+]
+
+
+@pytest.mark.parametrize("call,kw", OVERLAPPING)
+def test_overlapping_buffers_are_refused(L, call, kw):
+    assert apart(call, L, **kw) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: only where no device can run the call")
+@pytest.mark.parametrize("call,kw", BESIDE)
+def test_buffers_beside_each_other_are_not_refused(L, call, kw):
+    assert apart(call, L, **kw) == NO_DEVICE
 
 
 def test_empty_calls_do_nothing(L):

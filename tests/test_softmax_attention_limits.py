@@ -221,3 +221,43 @@ def test_many_pages_past_32_bits(held, nodes, H):
     s = ((D + 8) * E * size + 8 * E)[..., None]
     u = half_step(BF)
     close(o, want, (u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())
+
+
+# ---------------------------------------------------------------- buffers that overlap
+
+def test_overlapping_tensors_are_refused():
+    """Outputs that lie on what is read, or on one another; in place and side by
+    side in one buffer they are fine."""
+    T, H, D = 6, 2, 64
+    w, pos, f = torch.ones(D, device=DEV), torch.arange(T, dtype=torch.int32, device=DEV), gdn.rope_inv_freq(32, device=DEV)
+    room = rnd(191, 6 * T, H, D, dtype=BF).to(DEV)
+    q, k, v, a, b = (room[i * T:(i + 1) * T] for i in range(5))
+    for kw in (dict(out_q=k), dict(out_k=q), dict(out_q=a, out_k=a), dict(out_q=room[1:T + 1]), dict(out_q=a, out_k=room[3 * T + 1:4 * T + 1])):
+        with pytest.raises(gdn.GDNError):
+            gdn.qk_norm_rope(q, k, w, w, pos, f, **kw)
+    want = gdn.qk_norm_rope(q, k, w, w, pos, f)
+    got = gdn.qk_norm_rope(q, k, w, w, pos, f, out_q=a, out_k=b)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    pool = Pool([20], [T], H, D, 16, BF, fill=192)
+    cache, pages = pool.cache, pool.where
+    for kw in (dict(out_q=k), dict(out_q=v), dict(out_q=room[1:T + 1]), dict(out_q=cache.k.view(-1)[:T * H * D].view(T, H, D))):
+        with pytest.raises(gdn.GDNError):
+            gdn.qk_norm_rope_cache(q, k, v, w, w, pos, f, cache, *pages, **kw)
+    with pytest.raises(gdn.GDNError):
+        gdn.kv_cache_write(cache.k.view(-1)[:T * H * D].view(T, H, D), v, cache, *pages)
+    with pytest.raises(gdn.GDNError):
+        gdn.kv_cache_write(k, v, cache._replace(v=cache.k), *pages)
+    with pytest.raises(gdn.GDNError):
+        gdn.kv_cache_read(cache, *pages, n_tokens=T, out_k=a, out_v=room[3 * T + 1:4 * T + 1])
+    lens = torch.tensor([20, 0], dtype=torch.int32, device=DEV)
+    with pytest.raises(gdn.GDNError):
+        gdn.kv_cache_accept(cache, pages[0], lens[:1], pages[2], torch.zeros((1, 1), dtype=torch.int32, device=DEV),
+                            out_seq_lens=pages[2][1:])
+    got = gdn.kv_cache_accept(cache, pages[0], lens[:1], pages[2], torch.zeros((1, 1), dtype=torch.int32, device=DEV),
+                              out_seq_lens=lens[1:])
+    assert lens.tolist() == [20, 15] and got.data_ptr() == lens[1:].data_ptr()
+    for kw in (dict(out=q), dict(out=room[1:T + 1]), dict(gate=v, out=v), dict(out=a, workspace=room.view(torch.uint8))):
+        with pytest.raises(gdn.GDNError):
+            gdn.tree_attention(q, cache, *pages, max_nodes=T, **kw)
+    want = gdn.tree_attention(q, cache, *pages, max_nodes=T)
+    assert torch.equal(gdn.tree_attention(q, cache, *pages, max_nodes=T, out=a), want)
