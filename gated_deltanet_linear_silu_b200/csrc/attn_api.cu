@@ -92,17 +92,35 @@ Span lens_of(const gdn::PageArgs& p) { return dense(p.lens, (int64_t)4 * p.N); }
 Span cu_of(const gdn::PageArgs& p) { return dense(p.cu, (int64_t)4 * (p.N + 1)); }
 bool overlaps_pages(const Span& out, const gdn::PageArgs& p) { return overlaps(out, table_of(p), lens_of(p), cu_of(p)); }
 
-gdn_status_t check_cache(const gdn_kv_cache_t* c, gdn::CacheView* out) {
+// What a cache's fields say without its memory; log2 of the page's tokens.
+gdn_status_t check_cache_shape(const gdn_kv_cache_t* c, int* page_shift) {
     if (!c || c->n_pages < 1 || c->Hk < 1) return GDN_ERR_INVALID_ARG;
     if (c->dtype != GDN_BF16 && c->dtype != GDN_E4M3) return GDN_ERR_INVALID_ARG;
     if (!row_dim_ok(c->D) || c->Hk > kMaxHeads) return GDN_ERR_UNSUPPORTED;
     int shift = 0;
     while ((1 << shift) < c->page && shift < 20) ++shift;
     if (c->page < 16 || c->page > 1024 || (1 << shift) != c->page) return GDN_ERR_UNSUPPORTED;
+    *page_shift = shift;
+    return GDN_OK;
+}
+
+gdn_status_t check_cache(const gdn_kv_cache_t* c, gdn::CacheView* out) {
+    int shift = 0;
+    if (gdn_status_t st = check_cache_shape(c, &shift)) return st;
     if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return GDN_ERR_INVALID_ARG;
     if (c->dtype == GDN_E4M3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
         return GDN_ERR_INVALID_ARG;
     *out = gdn::CacheView{c->k, c->v, c->k_scale, c->v_scale, c->n_pages, shift, c->Hk, c->D, c->dtype == GDN_E4M3};
+    return GDN_OK;
+}
+
+// The tree attention's sizes, for a cache that check_cache_shape allows.
+gdn_status_t check_tree(const gdn_kv_cache_t* c, int page_shift, int N, int H, int max_nodes) {
+    if (N < 0 || H < 1 || H % c->Hk != 0 || max_nodes < 1) return GDN_ERR_INVALID_ARG;
+    if (max_nodes > gdn::kMaxNodes || H / c->Hk > 64) return GDN_ERR_UNSUPPORTED;
+    if (!(c->D == 64 || c->D == 128 || c->D == 256)) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)N * c->Hk >= (int64_t)1 << 31) return GDN_ERR_UNSUPPORTED;
+    if (c->n_pages >= ((int64_t)1 << 31) / ((int64_t)c->Hk << page_shift)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -257,10 +275,8 @@ gdn_status_t gdn_kv_accept(const gdn_kv_cache_t* cache, const int32_t* page_tabl
 }
 
 size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, int N, int H, int max_nodes) {
-    if (!cache || N < 0 || H <= 0 || cache->Hk <= 0 || cache->Hk > kMaxHeads || H % cache->Hk != 0 ||
-        H / cache->Hk > 64 || max_nodes <= 0 || max_nodes > gdn::kMaxNodes ||
-        !(cache->D == 64 || cache->D == 128 || cache->D == 256))
-        return 0;
+    int shift = 0;
+    if (check_cache_shape(cache, &shift) != GDN_OK || check_tree(cache, shift, N, H, max_nodes) != GDN_OK) return 0;
     const size_t b = gdn::tree_workspace_bytes(N, H, cache->Hk, cache->D, max_nodes, cache->dtype == GDN_E4M3);
     return (b + 255) / 256 * 256;
 }
@@ -274,11 +290,9 @@ gdn_status_t gdn_tree_attention(const void* q, gdn_dtype_t dtype, int64_t T, int
     gdn::TreeArgs a{};
     if (gdn_status_t st = check_cache(cache, &a.c)) return st;
     if (gdn_status_t st = check_pages(page_table, max_pages, seq_lens, cu_seqlens, N, T, &a.p)) return st;
-    if (H < 1 || H % a.c.Hk != 0 || max_nodes < 1 || !(scale > 0.f) || !(scale <= 3.4e38f)) return GDN_ERR_INVALID_ARG;
-    if (dtype != GDN_BF16 || max_nodes > gdn::kMaxNodes) return GDN_ERR_UNSUPPORTED;
-    if (!(a.c.D == 64 || a.c.D == 128 || a.c.D == 256) || H / a.c.Hk > 64) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)N * a.c.Hk >= (int64_t)1 << 31) return GDN_ERR_UNSUPPORTED;
-    if (a.c.n_pages >= ((int64_t)1 << 31) / ((int64_t)a.c.Hk << a.c.page_shift)) return GDN_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !(scale <= 3.4e38f)) return GDN_ERR_INVALID_ARG;
+    if (gdn_status_t st = check_tree(cache, a.c.page_shift, N, H, max_nodes)) return st;
+    if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
     if (T == 0) return GDN_OK;
     if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || !aligned(gate, 16) || !aligned(mask, 8) || !aligned(lse, 4))
         return GDN_ERR_INVALID_ARG;

@@ -228,6 +228,20 @@ def test_buffers_beside_each_other_are_not_refused(L, call, kw):
     assert apart(call, L, **kw) == NO_DEVICE
 
 
+@pytest.mark.parametrize("kw", [kw for kw, _ in BAD_CACHE if not {"k", "v", "k_scale", "v_scale"} & set(kw)] + [
+    dict(dtype=7), dict(n_pages=1 << 27), dict(n_pages=(1 << 31) // 32), dict(D=96), dict(Hk=1 << 17)])
+def test_workspace_size_of_unsupported_caches(L, kw):
+    """0 for every cache that the attention refuses, whatever its memory."""
+    assert L.gdn_tree_attention_workspace_size(cache(**kw), 1, 4 * kw.get("Hk", 2) or 4, 2) == 0
+    empty = dict(k=None, v=None, k_scale=None, v_scale=None)
+    assert L.gdn_tree_attention_workspace_size(cache(**empty), 1, 4, 2) > 0
+
+
+def test_workspace_size_of_too_many_units(L):
+    size = lambda N: L.gdn_tree_attention_workspace_size(cache(Hk=1 << 16, n_pages=1), N, 1 << 16, 2)
+    assert size(1) > 0 and size(1 << 15) == 0
+
+
 def test_empty_calls_do_nothing(L):
     empty = dict(N=0, table=None, lens=None, cu=None)
     assert norm_rope(L, T=0, q=None, k=None) == OK
