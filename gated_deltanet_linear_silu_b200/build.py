@@ -53,8 +53,26 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def binding_tag() -> str:
+    """What a binding is compiled against: PyTorch's C++ classes and Python's. It
+    stands in the module (gdn_binding_tag), since one built for others may load
+    and take a tensor's fields from the wrong places."""
+    import sysconfig
+
+    import torch
+
+    return (f"gdn binding for torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"{sysconfig.get_config_var('SOABI')}")
+
+
+def binding_matches() -> bool:
+    """Whether _binding.so was built for this PyTorch and this Python."""
+    with open(BINDING, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "gdn.h"), os.path.abspath(__file__)])
+    return _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "gdn.h"), os.path.abspath(__file__)]) and binding_matches()
 
 
 def build_binding() -> str:
@@ -73,6 +91,7 @@ def build_binding() -> str:
     tmp = BINDING + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DGDN_BINDING_TAG="{binding_tag()}"',
            *[x for i in inc for x in ("-isystem", i)], BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -20,6 +20,9 @@
 
 #include "../../include/gdn.h"
 
+// What this was compiled against (build.py looks for it in the file).
+extern "C" __attribute__((used, visibility("default"))) const char gdn_binding_tag[] = GDN_BINDING_TAG;
+
 namespace {
 
 struct Entry {

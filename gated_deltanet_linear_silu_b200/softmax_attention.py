@@ -32,6 +32,11 @@ def _binding():
     if _bound is None:
         if not os.path.exists(os.path.join(_HERE, "_binding.so")):
             raise RuntimeError("_binding.so is missing: build it with `python -m gated_deltanet_linear_silu_b200.build`")
+        from . import build
+
+        if not build.binding_matches():  # (before it is loaded)
+            raise RuntimeError(f"_binding.so is not the {build.binding_tag()}: "
+                               "build it with `python -m gated_deltanet_linear_silu_b200.build`")
         library = lib()  # refuses another ABI version
         module = importlib.import_module("._binding", __package__)
         module.bind(*(ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in _ENTRIES), GDNError)

@@ -288,6 +288,27 @@ def test_binding_refuses_tensors(L):
     assert f8 == held.k.dtype
 
 
+@pytest.mark.parametrize("what", ["torch", "abi", "python"])
+def test_binding_for_another_torch_or_python_is_stale(L, monkeypatch, what):
+    """The binding is compiled against one PyTorch's classes and one Python's: for
+    others it is built again, and not loaded before."""
+    from gated_deltanet_linear_silu_b200 import softmax_attention
+
+    assert gbuild.binding_up_to_date()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    elif what == "abi":
+        monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    else:
+        import sysconfig
+        config = sysconfig.get_config_var
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else config(name))
+    assert not gbuild.binding_up_to_date()
+    monkeypatch.setattr(softmax_attention, "_bound", None)
+    with pytest.raises(RuntimeError, match="build"):
+        softmax_attention._binding()
+
+
 def test_tree_mask():
     #   0        0
     #  / \       |
