@@ -86,6 +86,9 @@ __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Positions are counted in 32 bits, a few tiles past a sequence's end as well.
+constexpr int kMaxLen = 0x7FFFFFFF - 1023;
+
 // Sequence n's draft and length, checked; no nodes where there is nothing to do.
 struct Seq {
     int first, nodes, len;  // first packed token, drafted tokens, cached tokens
@@ -97,7 +100,7 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int n) {
     const int64_t end = a.p.cu[n + 1], nodes = end - q.first;
     q.len = a.p.lens[n];
     q.bad = q.first < 0 || nodes < 0 || end > a.T || nodes > a.max_nodes || q.len < nodes ||
-            q.len > ((int64_t)a.p.max_pages << a.c.page_shift);
+            q.len > ((int64_t)a.p.max_pages << a.c.page_shift) || q.len > kMaxLen;
     q.nodes = q.bad ? 0 : (int)nodes;
     return q;
 }

@@ -597,7 +597,8 @@ GDN_API size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, in
  *   workspace  ws_bytes >= gdn_tree_attention_workspace_size(...), 256-byte
  *              aligned; calls that may overlap need one each
  * Supported: bf16, D 64, 128 or 256, up to 64 query heads per key/value head,
- * caches of fewer than 2^31 rows (n_pages * Hk * page).
+ * caches of fewer than 2^31 rows (n_pages * Hk * page). A sequence of more than
+ * 2^31 - 1024 cached positions is skipped and sets the device status word.
  */
 GDN_API gdn_status_t gdn_tree_attention(const void* q, gdn_dtype_t dtype, int64_t T, int64_t ld_q, int H,
                                         const gdn_kv_cache_t* cache, const int32_t* page_table, int max_pages,

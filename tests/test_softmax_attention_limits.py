@@ -261,3 +261,23 @@ def test_overlapping_tensors_are_refused():
             gdn.tree_attention(q, cache, *pages, max_nodes=T, **kw)
     want = gdn.tree_attention(q, cache, *pages, max_nodes=T)
     assert torch.equal(gdn.tree_attention(q, cache, *pages, max_nodes=T, out=a), want)
+
+
+# ---------------------------------------------------------------- lengths
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("heads", [4, 32])  # either kernel
+def test_tree_attention_refuses_lengths_next_to_32_bits(held, heads):
+    """A length whose last tile would end past 2^31 is skipped and reported; the
+    other sequence is done."""
+    pool = Pool([40, 70], [1, 1], 1, 64, 1024, held, fill=201)
+    wide = torch.zeros((2, 1 << 21), dtype=torch.int32, device=DEV)  # 2^31 positions of pages that exist
+    wide[1, 0] = int(pool.ids[1, 0])
+    q = rnd(202, 2, heads, 64, dtype=BF).to(DEV)
+    for length in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 1023):
+        pool.lens[0] = length
+        out = torch.full(q.shape, 7.0, dtype=BF, device=DEV)
+        o, lse = gdn.tree_attention(q, pool.cache, wide, pool.lens, pool.cu, max_nodes=1, out=out, return_lse=True)
+        status_bad()
+        assert (o[0] == 7).all()
+        check_attention(pool, q, o, lse, None, 0.125, rows=[1])
