@@ -30,7 +30,8 @@
 //
 // e4m3 values enter the products as f16, exactly, by the hardware conversion
 // (one instruction for two; through bf16 it would take five), and so do the
-// queries, each row scaled by a power of two into f16's range. Keys' scales
+// queries, each row scaled by a power of two that leaves f16 as many bits as it has
+// (exact down to 2^-31 of the row's largest element, off by 2^-39 of it below). Keys' scales
 // multiply the scores in fp32. Values' scales multiply the probabilities; the
 // running reference R of a row is over s_j + log2 vs_j, so that the largest
 // weight e^{s - R} vs is about one and f16 (11 bits) holds the others next to
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
             const bool live = 8 * g + r < rows;
             const int64_t t = seq.first + (live ? 8 * g + r : 0) / G;
             const uint16_t* qp = static_cast<const uint16_t*>(a.q) + t * a.ld_q + (int64_t)(hk * G + (live ? 8 * g + r : 0) % G) * D;
-            float down = 1.f, up = 1.f;  // the row's power of two, so that its largest element is in [1, 2)
+            float down = 1.f, up = 1.f;  // the row's power of two (query_scale)
             if (E4M3) {
                 uint32_t m = 0;
 #pragma unroll
@@ -209,10 +210,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 }
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                uint32_t e = m >> 7;  // 127 + exponent; a row that is not finite stays as it is
-                e = e == 255u || m == 0u ? 127u : e < 1u ? 1u : e > 253u ? 253u : e;
-                down = __uint_as_float((254u - e) << 23);
-                up = __uint_as_float(e << 23);
+                query_scale(m, down, up);
             }
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {

@@ -54,6 +54,18 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
     return y;
 }
 
+// The power of two that takes a row of bf16 queries to f16, and back: it puts the
+// largest magnitude, whose bits are `top`, in [2^14, 2^15). The least that f16 keeps is
+// 2^-24, so that an element's eight bits are exact down to 2^-31 of the largest, and
+// what is below is off by 2^-39 of it at most: less than the fp32 sums of the scores.
+// Rows below 2^-112 stay lower; the finite elements of one that is not finite fit.
+__device__ __forceinline__ void query_scale(uint32_t top, float& down, float& up) {
+    uint32_t e = top >> 7;  // 127 + exponent
+    e = e < 15u ? 15u : e > 254u ? 254u : e;
+    down = __uint_as_float((268u - e) << 23);
+    up = __uint_as_float((e - 14u) << 23);
+}
+
 // log2 of a value row's scale for the running reference: at least -100, so that
 // a weight without its scale stays in fp32's range.
 __device__ __forceinline__ float log2_scale(float x) {

@@ -560,7 +560,7 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                 for (int e = 0; e < D / 16; ++e) u[e] = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
                 float down = 1.f;
                 if (E4M3) {
-                    // as f16, the row scaled by a power of two that puts its largest element in [1, 2)
+                    // as f16, the row scaled by a power of two
                     uint32_t big = 0;
 #pragma unroll
                     for (int e = 0; e < D / 16; ++e) {
@@ -571,10 +571,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                     row_top[half * 128 + m] = __uint_as_float(big);
                     pair_sync(pair);
                     big = max(big, __float_as_uint(row_top[(half ^ 1) * 128 + m]));
-                    uint32_t ex = big >> 7;  // a row that is not finite stays as it is
-                    ex = ex == 255u || big == 0u ? 127u : ex < 1u ? 1u : ex > 253u ? 253u : ex;
-                    down = __uint_as_float((254u - ex) << 23);
-                    mul *= __uint_as_float(ex << 23);
+                    float up;
+                    query_scale(big, down, up);
+                    mul *= up;
                 }
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {

@@ -582,7 +582,8 @@ GDN_API size_t gdn_tree_attention_workspace_size(const gdn_kv_cache_t* cache, in
  * does not reach it, whatever it holds (infinities and NaN included). fp32
  * accumulation; for the products the softmax's numerators are rounded to the
  * type that the values take there: bf16 from a bf16 cache, f16 (11 bits) from an
- * e4m3 one, whose scales are applied in fp32. A sequence with a position whose
+ * e4m3 one, whose scales are applied in fp32 (its queries are f16 as well, exact
+ * down to 2^-31 of a row's largest element). A sequence with a position whose
  * page does not exist is computed with other rows in its place: its output means
  * nothing. The result does not depend on what else runs, and for one
  * set of arguments is the same bits at every call.

@@ -281,3 +281,29 @@ def test_tree_attention_refuses_lengths_next_to_32_bits(held, heads):
         status_bad()
         assert (o[0] == 7).all()
         check_attention(pool, q, o, lse, None, 0.125, rows=[1])
+
+
+# ---------------------------------------------------------------- f16 operands of an e4m3 cache
+
+@pytest.mark.parametrize("held", [F8, BF])
+@pytest.mark.parametrize("heads", [4, 32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("log2_outlier", [12, 17, 20, 24])
+def test_tree_attention_beside_an_outlier_in_the_queries(heads, D, log2_outlier, held):
+    """A query element far above the others, at a channel where the keys are zero:
+    the scores are the other elements', to all their bits."""
+    L = 300
+    pool = Pool([L], [1], 1, D, 16, held)
+    k, v = rnd(221, L, 1, D), rnd(222, L, 1, D)
+    k[..., 5] = 0
+    whole = (pool.table, pool.lens, torch.tensor([0, L], dtype=torch.int32, device=DEV))
+    gdn.kv_cache_write(k.to(DEV), v.to(DEV), pool.cache, *whole)
+    q = rnd(223, 1, heads, D, dtype=BF)
+    q[..., 5] = 2.0 ** log2_outlier
+    q = q.to(DEV)
+    o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=1, return_lse=True)
+    k, v = (pool.rows(0, range(L), name) for name in ("k", "v"))
+    want, z, mass, size = ref.attention(q.cpu(), k, v, L - 1, [1], D ** -0.5)
+    s, u = ((D + 8) * E * size + 8 * E)[..., None], half_step(BF)
+    close(o, want, (u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())
+    close(lse, z, s[..., 0] + 16 * E * (1 + z.abs()))  # (300 additions of a row: under a dozen to a chain)
