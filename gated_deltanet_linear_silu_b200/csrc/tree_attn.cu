@@ -34,9 +34,11 @@
 // (exact down to 2^-31 of the row's largest element, off by 2^-39 of it below). Keys' scales
 // multiply the scores in fp32. Values' scales multiply the probabilities; the
 // running reference R of a row is over s_j + log2 vs_j, so that the largest
-// weight e^{s - R} vs is about one and f16 (11 bits) holds the others next to
+// weight e^{s - R} vs is 2^7 and f16 (11 bits) holds the others next to
 // it, however the scales differ. R moves, and the sums are rescaled, only when
-// a weight would pass 2^8. Sums, maxima and outputs are fp32.
+// a weight would pass 2^15 (bf16: one, and 2^8). Sums, maxima and outputs are fp32.
+// From a bf16 cache the numerators are bf16, since both operands of a product have one
+// type: 8 bits, half a step of each, where fp32 ones would take three products for one.
 #include <cfloat>
 
 #include "kv_page.cuh"
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                         if (E4M3) s[g][e] *= ks[e >> 1];
                         t[g][e] = E4M3 ? fmaf(s[g][e], mul[g][e & 1], lv[e >> 1]) : s[g][e] * mul[g][e & 1];
                         if (!seen(g, e)) t[g][e] = kNegInf;
-                        grown = grown || t[g][e] > ref[g][e & 1] + kLazy;
+                        grown = grown || t[g][e] > ref[g][e & 1] + (kLazy + kLift<E4M3>);
                     }
                 if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -361,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            top -= kLift<E4M3>;
                             const float old = ref[g][i];
                             if (!(top > old)) continue;
                             ref[g][i] = top;

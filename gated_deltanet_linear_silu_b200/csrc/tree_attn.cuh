@@ -28,6 +28,12 @@ struct Bool {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;  // growth of a row's largest weight (log2) that moves its reference
+// Where a move puts the largest weight (log2). f16 numerators (e4m3 caches) stand as
+// high as the growth and the type's 2^16 allow: they keep eleven bits down to 2^-21 of
+// the largest, and what is below is off by 2^-32 of it at most, so that 2^17 tokens of
+// such weights together move a sum by 2^-15 of its largest term.
+template <bool E4M3>
+constexpr float kLift = E4M3 ? 7.f : 0.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
@@ -66,12 +72,13 @@ __device__ __forceinline__ void query_scale(uint32_t top, float& down, float& up
     up = __uint_as_float((e - 14u) << 23);
 }
 
-// log2 of a value row's scale for the running reference: at least -100, so that
-// a weight without its scale stays in fp32's range.
+// log2 of a value row's scale for the running reference: at least -92, so that a
+// weight without its scale, up to 2^(92 + kLift + kLazy), and 2^20 of them stay in
+// fp32's range.
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return fmaxf(y, -100.f);
+    return fmaxf(y, -92.f);
 }
 
 // Zeroes the halves of a bf16 pair that are not finite; true if there was one.

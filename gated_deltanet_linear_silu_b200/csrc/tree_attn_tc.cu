@@ -653,8 +653,9 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                             top = fmaxf(top, top_b);
                             if (!E4M3) top *= mul;  // (the scale is positive)
                             // ---- the reference: moved when outgrown
-                            const bool move = top > ref + kLazy;
+                            const bool move = top > ref + (kLazy + kLift<E4M3>);
                             if (__any_sync(0xffffffffu, move)) {
+                                top -= kLift<E4M3>;
                                 const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
                                 if (move) ref = top;
                                 if (x != first && __any_sync(0xffffffffu, f != 1.f)) {
@@ -779,13 +780,13 @@ tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUten
                         top = fmaxf(top, top_b);
                         // ---- the reference: moved when either half outgrows it (both warps have
                         // read their scores when the vote is out: probabilities may overwrite them)
-                        if (pair_any(pair, !ok || (live && top > ref + kLazy))) {
+                        if (pair_any(pair, !ok || (live && top > ref + (kLazy + kLift<E4M3>)))) {
                             row_top[half * 128 + m] = top;
                             if (!ok) B.gave_up[warp] = 1;
                             pair_sync(pair);
                             ok = ok && !B.gave_up[warp ^ 4];
                             if (!ok) break;
-                            top = fmaxf(top, row_top[(half ^ 1) * 128 + m]);
+                            top = fmaxf(top, row_top[(half ^ 1) * 128 + m]) - kLift<E4M3>;
                             const bool move = top > ref;
                             const float f = move && ref != kNegInf ? exp2_approx(ref - top) : 1.f;
                             if (move) ref = top;

@@ -307,3 +307,47 @@ def test_tree_attention_beside_an_outlier_in_the_queries(heads, D, log2_outlier,
     s, u = ((D + 8) * E * size + 8 * E)[..., None], half_step(BF)
     close(o, want, (u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs())
     close(lse, z, s[..., 0] + 16 * E * (1 + z.abs()))  # (300 additions of a row: under a dozen to a chain)
+@pytest.mark.parametrize("heads", [4, 32])  # either kernel
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("log2_ratio", [-14.3, -17.2, -20.6])
+def test_tree_attention_beside_a_dominating_token(heads, D, log2_ratio):
+    """One context token takes nearly all of a row's weight but holds a value in one
+    element only: the others' sums, all of small numerators that round alike, keep
+    their bits. (The numerators are at least 2^-21 of the largest: eleven bits in f16
+    where that is at least 2^7, ten where they reach below the normal range; the
+    tolerance counts eight.)"""
+    L, N = 192, 1200  # as many sequences, all on the same pages, as leave most of them whole to a CTA
+    pool = Pool([L], [1], 1, D, 32, F8)
+    k, v = torch.zeros(L, 1, D), rnd(211, 1, 1, D).repeat(L, 1, 1)
+    k[20, 0, 0] = -log2_ratio * math.log(2) / D ** -0.5
+    v[20] = 0
+    v[20, 0, 0] = float(v[0].abs().max())
+    whole = (pool.table, pool.lens, torch.tensor([0, L], dtype=torch.int32, device=DEV))
+    gdn.kv_cache_write(k.to(DEV), v.to(DEV), pool.cache, *whole)
+    q = torch.zeros(N, heads, D, dtype=BF, device=DEV)
+    q[..., 0] = 1
+    o, lse = gdn.tree_attention(q, pool.cache, pool.table.repeat(N, 1), pool.lens.repeat(N),
+                                torch.arange(N + 1, dtype=torch.int32, device=DEV), max_nodes=1, return_lse=True)
+    k, v = (pool.rows(0, range(L), name) for name in ("k", "v"))
+    want, z, mass, size = ref.attention(q[:1].cpu(), k, v, L - 1, [1], D ** -0.5)
+    s, u = ((D + 8) * E * size + 8 * E)[..., None], half_step(BF)
+    close(o, want.expand(N, -1, -1), ((u + 2 * s + 2.0 ** -9) * mass * (1 + u) + u * want.abs()).expand(N, -1, -1))
+    close(lse, z.expand(N, -1), (s[..., 0] + 16 * E * (1 + z.abs())).expand(N, -1))
+
+
+
+
+@pytest.mark.parametrize("heads", [4, 32])
+def test_tree_attention_over_values_of_all_sizes(heads):
+    """Rows of values that are zero, of ordinary size, tiny and huge: the reference
+    follows their scales, the weights without them stay finite."""
+    L, D = 3000, 128
+    for sizes in ((0.0,), (0.0, 1.0), (1e-30, 1e30), (1e-38, 1.0, 0.0), (3e38, 1e-3)):
+        pool = Pool([L], [1], 1, D, 32, F8)
+        k, v = rnd(231, L, 1, D), rnd(232, L, 1, D).clamp(-1, 1)
+        v *= torch.tensor([sizes[i * 7919 % len(sizes)] for i in range(L)])[:, None, None]
+        whole = (pool.table, pool.lens, torch.tensor([0, L], dtype=torch.int32, device=DEV))
+        gdn.kv_cache_write(k.to(DEV), v.to(DEV), pool.cache, *whole)
+        q = rnd(233, 1, heads, D, dtype=BF).to(DEV)
+        o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=1, return_lse=True)
+        check_attention(pool, q, o, lse, None, D ** -0.5)
