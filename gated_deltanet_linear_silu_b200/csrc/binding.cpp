@@ -59,6 +59,11 @@ int int32(PyObject* o, const char* name) {
     if (x < INT32_MIN || x > INT32_MAX) value_error(std::string(name) + " does not fit 32 bits");
     return (int)x;
 }
+bool truth(PyObject* o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw Refused{nullptr, ""};
+    return x != 0;
+}
 double real(PyObject* o) {
     const double x = PyFloat_AsDouble(o);
     if (x == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
@@ -255,7 +260,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const On on(dev);
         check(g.qk_norm_rope(q.data_ptr(), k.data_ptr(), type, q.size(0), (int)q.size(1), (int)k.size(1),
                              (int)q.size(2), ld_q, ld_k, m.q_w, m.k_w, (float)real(a[6]), m.pos, m.inv_freq, m.rotary,
-                             PyObject_IsTrue(a[7]), oq.data_ptr(), ok.data_ptr(), on.stream),
+                             truth(a[7]), oq.data_ptr(), ok.data_ptr(), on.stream),
               "gdn_qk_norm_rope");
         return pair(oq, ok);
     });
@@ -277,7 +282,7 @@ PyObject* qk_norm_rope_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const On on(dev);
         check(g.qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), type, q.size(0), (int)q.size(1), ld_q, ld_k,
                                    ld_v, m.q_w, m.k_w, (float)real(a[14]), m.pos, m.inv_freq, m.rotary,
-                                   PyObject_IsTrue(a[15]), &c.c, p.table, p.max_pages, p.lens, p.cu, p.N, oq.data_ptr(),
+                                   truth(a[15]), &c.c, p.table, p.max_pages, p.lens, p.cu, p.N, oq.data_ptr(),
                                    on.stream),
               "gdn_qk_norm_rope_cache");
         return THPVariable_Wrap(oq);
@@ -312,7 +317,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Pages p(a + 4, dev);
         const int64_t T = integer(a[7]);
         if (T < 0) value_error("n_tokens must not be negative");
-        const bool bf16 = PyObject_IsTrue(a[8]);
+        const bool bf16 = truth(a[8]);
         const int64_t shape[3] = {T, c.c.Hk, c.c.D};
         const at::ScalarType type = bf16 ? at::kBFloat16 : at::kFloat;
         const at::Tensor k = output(a[9], shape, type, dev, "out_k"), v = output(a[10], shape, type, dev, "out_v");
@@ -368,7 +373,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const float scale = a[10] == Py_None ? 1.f / std::sqrt((float)c.c.D) : (float)real(a[10]);
         const at::Tensor o = output(a[13], q.sizes(), q.scalar_type(), dev, "out");
-        const bool want_lse = PyObject_IsTrue(a[12]);
+        const bool want_lse = truth(a[12]);
         at::Tensor lse;
         const int64_t lse_shape[2] = {T, H};
         if (want_lse) lse = empty(lse_shape, at::kFloat, dev);

@@ -351,3 +351,20 @@ def test_tree_attention_over_values_of_all_sizes(heads):
         q = rnd(233, 1, heads, D, dtype=BF).to(DEV)
         o, lse = gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=1, return_lse=True)
         check_attention(pool, q, o, lse, None, D ** -0.5)
+
+
+# ---------------------------------------------------------------- odd Python arguments
+
+def test_flags_without_a_truth_value():
+    """What has no truth value raises its own error, and no result comes with it."""
+    T, H, D = 2, 2, 64
+    q, w = rnd(241, T, H, D, dtype=BF).to(DEV), torch.ones(D, device=DEV)
+    pos, f = torch.arange(T, dtype=torch.int32, device=DEV), gdn.rope_inv_freq(32, device=DEV)
+    pool = Pool([20], [T], H, D, 16, BF, fill=242)
+    both = torch.ones(2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gdn.qk_norm_rope(q, q.clone(), w, w, pos, f, interleaved=both)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gdn.qk_norm_rope_cache(q, q.clone(), q.clone(), w, w, pos, f, pool.cache, *pool.where, interleaved=both)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=T, return_lse=both)
