@@ -164,6 +164,8 @@ struct Norm {
         if (q.dim() != 3 || k.dim() != 3 || k.size(0) != q.size(0) || k.size(2) != q.size(2) ||
             k.scalar_type() != q.scalar_type())
             value_error("q must be [T, H, D] and k [T, Hk, D] of one dtype");
+        if (q.size(1) > INT32_MAX || k.size(1) > INT32_MAX || q.size(2) > INT32_MAX)
+            value_error("q, k: more heads or elements than 32 bits count");
         const at::Tensor &wq = tensor(a[0], "q_w"), &wk = tensor(a[1], "k_w"), &p = tensor(a[2], "positions"),
                          &f = tensor(a[3], "inv_freq");
         if (wq.dim() != 1 || wq.size(0) != q.size(2) || wk.dim() != 1 || wk.size(0) != q.size(2) ||

@@ -368,3 +368,14 @@ def test_flags_without_a_truth_value():
         gdn.qk_norm_rope_cache(q, q.clone(), q.clone(), w, w, pos, f, pool.cache, *pool.where, interleaved=both)
     with pytest.raises(RuntimeError, match="ambiguous"):
         gdn.tree_attention(q, pool.cache, *pool.where, max_nodes=T, return_lse=both)
+
+
+def test_head_counts_past_32_bits_are_refused():
+    """Counted in 32 bits by the C ABI: 2^32 + 2 heads must not pass as two. (No
+    tokens, so that there is nothing to allocate.)"""
+    w, pos, f = torch.ones(64, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV), gdn.rope_inv_freq(32, device=DEV)
+    many, two = (torch.empty((0, h, 64), dtype=BF, device=DEV) for h in ((1 << 32) + 2, 2))
+    assert gdn.qk_norm_rope(two, two, w, w, pos, f)[0].shape == (0, 2, 64)
+    for q, k in ((many, two), (two, many)):
+        with pytest.raises(ValueError):
+            gdn.qk_norm_rope(q, k, w, w, pos, f)
