@@ -197,6 +197,8 @@ rows_kernel(RowsArgs a, int share_shift) {
         int64_t where = 0;
         if (MODE != kNormRope) {
             where = token_row(a.p, a.c, t);
+            // (sequences that reach past the last packed row: it is written up to there)
+            if (t == 0 && lane == 0 && a.p.cu[a.p.N] > a.T) set_status(a.status, kStatusBadSeqlens);
             if (where < 0) {
                 if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
                 continue;

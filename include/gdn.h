@@ -480,10 +480,11 @@ GDN_API gdn_status_t gdn_gated_rmsnorm(const void* y, const void* z, const float
  * all on the device. Packed rows behind cu_seqlens[N] are left as they are: not
  * read into the cache, nor written in the outputs. A position whose page does
  * not exist (an id outside 0..n_pages-1, or past max_pages) and bounds that make
- * no sense set the device status word (GDN_ERR_INVALID_ARG); the tokens
- * concerned are skipped (gdn_tree_attention: see there) and everything else is
- * done. Sequences may share pages
- * that a call only reads; a page that a call writes belongs to one sequence.
+ * no sense (in a call that writes the cache or attends, also a cu_seqlens[N]
+ * above T) set the device status word (GDN_ERR_INVALID_ARG); the tokens concerned
+ * are skipped (gdn_tree_attention: see there) and everything else is done.
+ * Sequences may share pages that a call only reads; a page that a call writes
+ * belongs to one sequence.
  * What these calls write (outputs, the workspace, a cache that they write to) must
  * not overlap what they read, nor one another, but for the in-place forms that
  * gdn_qk_norm_rope allows: GDN_ERR_INVALID_ARG.

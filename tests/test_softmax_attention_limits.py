@@ -379,3 +379,29 @@ def test_head_counts_past_32_bits_are_refused():
     for q, k in ((many, two), (two, many)):
         with pytest.raises(ValueError):
             gdn.qk_norm_rope(q, k, w, w, pos, f)
+
+
+# ---------------------------------------------------------------- fewer rows than the bounds count
+
+@pytest.mark.parametrize("held", [F8, BF])
+def test_fewer_packed_rows_than_tokens_are_reported(held):
+    """Keys and values that end before cu_seqlens does: the rows that are there are
+    written, and that some are missing is reported."""
+    T, H, D = 12, 2, 64
+    k, v = (rnd(s, T, H, D, dtype=BF).to(DEV) for s in (251, 252))
+    w, f = torch.ones(D, device=DEV), gdn.rope_inv_freq(32, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    for fused in (False, True):
+        full, cut = (Pool([20, 30], [5, 7], H, D, 16, held, seed=2) for _ in range(2))
+        for pool, n in ((full, T), (cut, T - 3)):
+            if fused:
+                gdn.qk_norm_rope_cache(k[:n], k[:n], v[:n], w, w, pos[:n], f, pool.cache, *pool.where)
+            else:
+                gdn.kv_cache_write(k[:n], v[:n], pool.cache, *pool.where)
+            if pool is cut:
+                status_bad()
+            gdn.check_device_status(DEV)
+        for name in ("k", "v"):
+            assert torch.equal(cut.rows(0, range(15, 20), name), full.rows(0, range(15, 20), name))
+            assert torch.equal(cut.rows(1, range(23, 27), name), full.rows(1, range(23, 27), name))
+            assert (cut.rows(1, range(27, 30), name) == 0).all()
