@@ -20,8 +20,9 @@
 // Measured: norm and rotation of 16384 tokens, 8 + 2 heads of 256, bf16: 39 us
 // (168 MB, 4.3 TB/s); 32771 tokens of 8 heads of 128 into an e4m3 cache: 46 us
 // (203 MB, 4.4 TB/s); 131101 such tokens read back: 153 us (814 MB, 5.3 TB/s, 81 %
-// of a copy's rate). The first two are held by instructions (61 and 68 % of the
-// issue slots): with eight elements a lane they took 46 and 62 us.
+// of a copy's rate). The first two reach neither limit (61 and 68 % of the issue slots):
+// a warp asks for a token's rows when the one before is stored, and waits for them. With
+// eight elements a lane, and more instructions, they took 46 and 62 us.
 //
 // The angle's turns, pos * inv_freq / (2 pi), are taken in fp64 and reduced to
 // [-1/2, 1/2] there: in fp32 a position of 2^18 would lose 2^-6 of a radian.

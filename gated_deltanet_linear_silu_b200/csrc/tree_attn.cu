@@ -25,7 +25,7 @@
 //
 // One node there is 1.1 GB of cache in 184 to 194 us, 5.7 to 6.0 TB/s (87 to 92 %
 // of a copy's rate): HBM is nearly the bound, the rest is the instructions
-// between its loads. 9.8 us for one sequence of 1021 tokens are latency: bounds and
+// between its loads. 9.3 us for one sequence of 1021 tokens are latency: bounds and
 // shares 1 us, a page's id and its rows 3, the four warps' sums 1, the join 3.5.
 //
 // e4m3 values enter the products as f16, exactly, by the hardware conversion
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
             const float inv = mt == kNegInf && lt == 0.f ? 0.f : 1.f / lt;
             y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
             const int64_t out = (t * a.H + head) * D + d;
-            if (a.gate) {
+            if (a.gate) {  // (__expf is off by 2 + 1.16 |g| ulp: 2^-17 where the sigmoid nears zero, against bf16's 2^-9)
                 const float4 g = load4(static_cast<const uint16_t*>(a.gate) + out);
                 y.x /= 1.f + __expf(-g.x); y.y /= 1.f + __expf(-g.y);
                 y.z /= 1.f + __expf(-g.z); y.w /= 1.f + __expf(-g.w);

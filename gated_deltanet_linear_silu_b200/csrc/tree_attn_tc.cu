@@ -32,11 +32,11 @@
 // has to move, and only then exchange maxima and rescale the output.
 //
 // What bounds it. bf16, 8 sequences of 32768 tokens, 64 nodes, 4 x 8 heads of 128:
-// 288 to 296 us (950 TFLOP/s, and 3.7 TB/s of a cache that is read once), 905 cycles a
+// 284 to 296 us (950 TFLOP/s, and 3.7 TB/s of a cache that is read once), 905 cycles a
 // tile, all of them the issuing warp's: the products' 512 and three waits. The
-// exponentials, 16 a cycle and SM, would take 512. The same from e4m3: 345 us, the
+// exponentials, 16 a cycle and SM, would take 512. The same from e4m3: 342 us, the
 // converters'. Heads of 256 from e4m3 (24 ragged sequences up to 16389 tokens,
-// 17 nodes): 82 to 90 us, 2190 cycles a tile, 1300 of them the converters' stores and
+// 17 nodes): 81 to 90 us, 2190 cycles a tile, 1300 of them the converters' stores and
 // 900 their waits and hand-overs (shared memory alone needs 1200), and 8 us of
 // bounds, queries and output for each (sequence, head) that a CTA takes part in.
 //
