@@ -139,6 +139,8 @@ template <typename T, int LPR, int MODE, bool INTER>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (MODE == kCacheWrite ? 4 : 3) : 2)
 rows_kernel(RowsArgs a, int share_shift) {
     extern __shared__ __align__(16) float trig[];  // per warp: cos [half], sin [half]
+    // sequences that reach past the last packed row: written up to there
+    if (MODE != kNormRope && blockIdx.x == 0 && threadIdx.x == 0 && a.p.cu[a.p.N] > a.T) set_status(a.status, kStatusBadSeqlens);
     constexpr int RW = 32 / LPR;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, sub = lane / LPR;
@@ -198,8 +200,6 @@ rows_kernel(RowsArgs a, int share_shift) {
         int64_t where = 0;
         if (MODE != kNormRope) {
             where = token_row(a.p, a.c, t);
-            // (sequences that reach past the last packed row: it is written up to there)
-            if (t == 0 && lane == 0 && a.p.cu[a.p.N] > a.T) set_status(a.status, kStatusBadSeqlens);
             if (where < 0) {
                 if (where == kRowBad && lane == 0) set_status(a.status, kStatusBadSeqlens);
                 continue;
