@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
             for (int g = 0; g < NT; ++g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][g][e] = 0.f;
-        bool odd = false;  // a drafted value was not finite
+        bool odd = false;  // a value of a step with drafted tokens was not finite
 
         int st = 0;
         for (int tile = tile0; tile < tile1; ++tile) {
@@ -416,14 +416,12 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
                 }
                 if (!E4M3 && drafted) {
                     // a drafted value that is not finite must not reach the rows that do not see it:
-                    // zero here, added to the others at the end of the segment (the context's, which
-                    // every row sees, stay)
+                    // zero here, added to the others at the end of the segment (with the context's
+                    // values of this step)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (pos + 8 * (x >> 1) + C::token(2 * c + (x & 1)) < base) continue;
+                    for (int x = 0; x < 4; ++x)
 #pragma unroll
                         for (int w = 0; w < W; ++w) odd |= zero_non_finite(v[x][w]);
-                    }
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -510,11 +508,12 @@ __global__ void __launch_bounds__(kThreads, (Config<D, E4M3, NT>::kCtas)) tree_k
             const int node = row / G, head = hk * G + row % G;
             const int64_t t = seq.first + node;
             if (!E4M3 && any_odd) {
-                // drafted values that are not finite, for the rows that see them
+                // values that are not finite in the steps with drafted tokens, for the rows that see
+                // them: the context before the draft is every row's
                 const uint64_t bits = a.mask ? (uint64_t)a.mask[t] : (2ull << node) - 1;
-                const int from = max(base, tile0 * kTile), to = min(seq.len, tile1 * kTile);
+                const int from = max(base & ~15, tile0 * kTile), to = min(seq.len, tile1 * kTile);
                 for (int p = from; p < to; ++p) {
-                    if (!((bits >> (p - base)) & 1)) continue;
+                    if (p >= base && !((bits >> (p - base)) & 1)) continue;
                     const int64_t vr = page_row(a.p, a.c, seg.n, p);
                     if (vr < 0) continue;
                     const float4 z = load4(static_cast<const uint16_t*>(a.c.v) + (vr + head_rows) * D + d);
