@@ -18,8 +18,8 @@
 // in one lane and the rotation exchanges nothing.
 //
 // Measured: norm and rotation of 16384 tokens, 8 + 2 heads of 256, bf16: 39 us
-// (168 MB, 4.3 TB/s); 32771 tokens of 8 heads of 128 into an e4m3 cache: 46 us
-// (203 MB, 4.4 TB/s); 131101 such tokens read back: 153 us (814 MB, 5.3 TB/s, 81 %
+// (168 MB, 4.4 TB/s); 32771 tokens of 8 heads of 128 into an e4m3 cache: 45 us
+// (203 MB, 4.5 TB/s); 131101 such tokens read back: 153 us (814 MB, 5.3 TB/s, 81 %
 // of a copy's rate). The first two reach neither limit (61 and 68 % of the issue slots):
 // a warp asks for a token's rows when the one before is stored, and waits for them. With
 // eight elements a lane, and more instructions, they took 46 and 62 us.
